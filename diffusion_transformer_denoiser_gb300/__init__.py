@@ -18,6 +18,8 @@ __all__ = [
     "gemm_gated_residual", "gemm_silu_gate", "gemm_qkv_rope", "qk_norm_rope", "attention", "attention_workspace_size",
     "gated_add", "silu_gate",
     "device_error", "device_supported", "TENSORS", "TimestepModulation", "rope_tables", "time_advance",
+    "rope_axes_tables", "attention_lse", "attention_backward", "attention_backward_workspace_size",
+    "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -88,6 +90,7 @@ _SIGNATURES = {
     "mi_denoise_step": ([_P, ctypes.POINTER(SeqLayout), _P, _P, _P, _P, _P, _P, _I, _P, _F, _F, _P, _P, _SZ,
                          _P], _I),
     "mi_rope_tables": ([_I, _I, _I, _F, _P, _P, _P], _I),
+    "mi_rope_axes_tables": ([_P, _I, _I, ctypes.POINTER(_I), _F, _P, _P, _P], _I),
     "mi_tmod_init": ([ctypes.POINTER(_P), ctypes.POINTER(_TmodDesc)], _I),
     "mi_tmod_destroy": ([_P], None),
     "mi_tmod_workspace_size": ([_P, _I, ctypes.POINTER(_SZ)], _I),
@@ -102,6 +105,11 @@ _SIGNATURES = {
     "mi_attention": ([_P, _P, _P, _P, _P, _I, _I, _I, _P], _I),
     "mi_attention_workspace_size": ([_I, _I, _I, ctypes.POINTER(_SZ)], _I),
     "mi_attention_ws": ([_P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P], _I),
+    "mi_attention_lse": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P], _I),
+    "mi_attention_backward_workspace_size": ([_I, _I, _I, ctypes.POINTER(_SZ)], _I),
+    "mi_attention_backward": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P], _I),
+    "mi_qk_norm_rope_backward_workspace_size": ([_I, _I, _I, ctypes.POINTER(_SZ)], _I),
+    "mi_qk_norm_rope_backward": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _SZ, _P], _I),
     "mi_gated_add": ([_P, _P, _P, _I, _P, _I, _I, _I, _P], _I),
     "mi_silu_gate": ([_P, _P, _I, _I, _P], _I),
 }
@@ -145,6 +153,12 @@ def _ptr(t: Optional[torch.Tensor], dtype=None) -> Optional[int]:
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
     return t.data_ptr()
+
+
+def _sized(t: Optional[torch.Tensor], n: int, name: str):
+    """The library sees pointers only: a tensor with too few or too many elements is refused here."""
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
 
 
 _BF = torch.bfloat16
@@ -310,6 +324,17 @@ def rope_tables(text_pad, grid_h, grid_w, rope_cos, rope_sin, theta=10000.0, str
                                 _ptr(rope_sin, torch.float32), _stream(stream)))
 
 
+def rope_axes_tables(positions, axis_pairs, rope_cos, rope_sin, theta=10000.0, stream=None):
+    """Tables [rows, 64] of tokens with positions [rows, axes]; axis_pairs: rotary pairs of each axis, 64 in all."""
+    if positions.dim() != 2 or positions.shape[1] != len(axis_pairs):
+        raise ValueError(f"positions {tuple(positions.shape)} must be [rows, {len(axis_pairs)}], one column per axis")
+    rows, n = positions.shape
+    _sized(rope_cos, rows * 64, "rope_cos")
+    _sized(rope_sin, rows * 64, "rope_sin")
+    _check(lib().mi_rope_axes_tables(_ptr(positions, torch.float32), rows, n, (_I * n)(*axis_pairs), theta,
+                                     _ptr(rope_cos, torch.float32), _ptr(rope_sin, torch.float32), _stream(stream)))
+
+
 def time_advance(t, dt, stream=None):
     _check(lib().mi_time_advance(_ptr(t, torch.float32), t.numel(), dt, _stream(stream)))
 
@@ -371,6 +396,63 @@ def attention(qp, kp, qkv, key_mask, o, batch, seq, n_heads, stream=None, ws=Non
         _check(lib().mi_attention_ws(_ptr(qp, _BF), _ptr(kp, _BF), _ptr(qkv, _BF), _ptr(key_mask, torch.uint8),
                                      _ptr(o, _BF), batch, seq, n_heads, _ptr(ws, torch.uint8) if ws.numel() else None,
                                      ws.numel(), _stream(stream)))
+
+
+# ------------------------------------------------------------------------------- training pass
+def _train_sizes(batch, seq, n_heads, **tensors):
+    """Element counts of the training pass's tensors, by the suffix-free names of the calls' arguments."""
+    packed = batch * n_heads * seq * 128
+    sizes = {"qkv": 3 * packed, "dqkv": 3 * packed, "lse": batch * n_heads * seq, "key_mask": batch * seq}
+    for name, t in tensors.items():
+        _sized(t, sizes.get(name, packed), name)
+
+
+def attention_lse(qp, kp, qkv, key_mask, o, lse, batch, seq, n_heads, ws=None, stream=None):
+    """attention that also stores lse [batch, heads, seq] (fp32) for attention_backward; `ws` as for attention."""
+    _train_sizes(batch, seq, n_heads, qp=qp, kp=kp, qkv=qkv, key_mask=key_mask, o=o, lse=lse)
+    use_ws = ws is not None and ws.numel() > 0
+    _check(lib().mi_attention_lse(_ptr(qp, _BF), _ptr(kp, _BF), _ptr(qkv, _BF), _ptr(key_mask, torch.uint8), _ptr(o, _BF),
+                                  _ptr(lse, torch.float32), batch, seq, n_heads,
+                                  _ptr(ws, torch.uint8) if use_ws else None, ws.numel() if use_ws else 0,
+                                  _stream(stream)))
+
+
+def attention_backward_workspace_size(batch, seq, n_heads) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().mi_attention_backward_workspace_size(batch, seq, n_heads, ctypes.byref(n)))
+    return n.value
+
+
+def attention_backward(qp, kp, qkv, key_mask, o, lse, d_o, dqp, dkp, dqkv, batch, seq, n_heads, ws, stream=None):
+    """Gradients of attention_lse: dqp, dkp, and dv in the v columns of dqkv (its q and k columns are left alone)."""
+    _train_sizes(batch, seq, n_heads, qp=qp, kp=kp, qkv=qkv, key_mask=key_mask, o=o, lse=lse, d_o=d_o, dqp=dqp, dkp=dkp,
+                 dqkv=dqkv)
+    _check(lib().mi_attention_backward(_ptr(qp, _BF), _ptr(kp, _BF), _ptr(qkv, _BF), _ptr(key_mask, torch.uint8),
+                                       _ptr(o, _BF), _ptr(lse, torch.float32), _ptr(d_o, _BF), _ptr(dqp, _BF),
+                                       _ptr(dkp, _BF), _ptr(dqkv, _BF), batch, seq, n_heads, _ptr(ws, torch.uint8),
+                                       ws.numel(), _stream(stream)))
+
+
+def qk_norm_rope_backward_workspace_size(batch, seq, n_heads) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().mi_qk_norm_rope_backward_workspace_size(batch, seq, n_heads, ctypes.byref(n)))
+    return n.value
+
+
+def qk_norm_rope_backward(qkv, q_norm_w, k_norm_w, rope_cos, rope_sin, dqp, dkp, dqkv, dq_norm_w, dk_norm_w, batch, seq,
+                          n_heads, ws, eps=1e-6, rope_bstride=0, stream=None):
+    """Gradients of qk_norm_rope: the q and k columns of dqkv (its v columns are left alone) and the two gains' (fp32)."""
+    _train_sizes(batch, seq, n_heads, qkv=qkv, dqp=dqp, dkp=dkp, dqkv=dqkv)
+    for name, t in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w), ("dq_norm_w", dq_norm_w), ("dk_norm_w", dk_norm_w)):
+        _sized(t, 128, name)
+    for name, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)):
+        if t.numel() < (batch - 1) * rope_bstride + seq * 64:
+            raise ValueError(f"{name} has {t.numel()} elements, too few for {batch} tables {rope_bstride} apart")
+    _check(lib().mi_qk_norm_rope_backward(_ptr(qkv, _BF), _ptr(q_norm_w, _BF), _ptr(k_norm_w, _BF),
+                                          _ptr(rope_cos, torch.float32), _ptr(rope_sin, torch.float32), rope_bstride,
+                                          _ptr(dqp, _BF), _ptr(dkp, _BF), _ptr(dqkv, _BF),
+                                          _ptr(dq_norm_w, torch.float32), _ptr(dk_norm_w, torch.float32), batch, seq,
+                                          n_heads, eps, _ptr(ws, torch.uint8), ws.numel(), _stream(stream)))
 
 
 def gated_add(x, y, mod, gate_row, out, batch, seq, stream=None):

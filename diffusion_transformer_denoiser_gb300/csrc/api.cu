@@ -2,6 +2,7 @@
 // the launch sequence of a block forward and of a guided denoising step.
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -344,6 +345,7 @@ static mi_status block_forward_impl(mi_block* blk, int batch, int S, const void*
     aa.err = dev->err;
     aa.part = at_part;
     aa.count = at_count;
+    aa.lse = nullptr;
     e = mi::attention_launch(tq, tk, tv, aa, blk->num_sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   }
@@ -804,7 +806,8 @@ mi_status mi_qk_norm_rope(const void* qkv, const void* q_norm_w, const void* k_n
 }
 
 static mi_status attention_common(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, void* o,
-                                  int batch, int seq, int n_heads, void* ws, size_t ws_bytes, bool use_ws, void* stream) {
+                                  float* lse, int batch, int seq, int n_heads, void* ws, size_t ws_bytes, bool use_ws,
+                                  void* stream) {
   if (!qp || !kp || !qkv || !o) return fail(MI_ERR_INVALID_ARG, "null tensor argument");
   if (!aligned16(qp) || !aligned16(kp) || !aligned16(qkv) || !aligned16(o))
     return fail(MI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
@@ -837,6 +840,7 @@ static mi_status attention_common(const void* qp, const void* kp, const void* qk
   aa.err = dev->err;
   aa.part = nullptr;
   aa.count = nullptr;
+  aa.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (need > 0) {
     const size_t cb_bytes = mi::attention_count_bytes(batch, seq, n_heads);
@@ -851,7 +855,7 @@ static mi_status attention_common(const void* qp, const void* kp, const void* qk
 
 mi_status mi_attention(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, void* o, int batch,
                        int seq, int n_heads, void* stream) {
-  return attention_common(qp, kp, qkv, key_mask, o, batch, seq, n_heads, nullptr, 0, false, stream);
+  return attention_common(qp, kp, qkv, key_mask, o, nullptr, batch, seq, n_heads, nullptr, 0, false, stream);
 }
 
 mi_status mi_attention_workspace_size(int batch, int seq, int n_heads, size_t* bytes) {
@@ -866,7 +870,161 @@ mi_status mi_attention_workspace_size(int batch, int seq, int n_heads, size_t* b
 
 mi_status mi_attention_ws(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, void* o, int batch,
                           int seq, int n_heads, void* ws, size_t ws_bytes, void* stream) {
-  return attention_common(qp, kp, qkv, key_mask, o, batch, seq, n_heads, ws, ws_bytes, true, stream);
+  return attention_common(qp, kp, qkv, key_mask, o, nullptr, batch, seq, n_heads, ws, ws_bytes, true, stream);
+}
+
+namespace {
+
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+
+// The first n_out spans are outputs: none of them may overlap another span.
+bool any_overlap(const Span* v, int n_out, int n) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(v[i].at), b = reinterpret_cast<uintptr_t>(v[j].at);
+      if (v[j].at != nullptr && a < b + v[j].bytes && b < a + v[i].bytes) return true;
+    }
+  return false;
+}
+
+}  // namespace
+
+// Shapes of the training calls: their kernels count tiles, rows and grid blocks in 32 bits.
+static mi_status check_train_shape(int batch, int seq, int n_heads) {
+  if (batch <= 0 || seq <= 0 || n_heads <= 0) return fail(MI_ERR_INVALID_ARG, "batch, seq, n_heads must be positive");
+  if (seq > (1 << 20)) return fail(MI_ERR_UNSUPPORTED, "seq=%d: at most 2^20 rows", seq);
+  if (n_heads > 1024) return fail(MI_ERR_UNSUPPORTED, "n_heads=%d: at most 1024", n_heads);
+  if ((long long)batch * seq * n_heads > (1LL << 30))
+    return fail(MI_ERR_UNSUPPORTED, "batch * seq * n_heads = %lld: at most 2^30", (long long)batch * seq * n_heads);
+  return MI_OK;
+}
+
+mi_status mi_attention_lse(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, void* o, float* lse,
+                           int batch, int seq, int n_heads, void* ws, size_t ws_bytes, void* stream) {
+  if (!lse) return fail(MI_ERR_INVALID_ARG, "null tensor argument");
+  if (!aligned16(lse)) return fail(MI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  mi_status st = check_train_shape(batch, seq, n_heads);
+  if (st != MI_OK) return st;
+  const size_t rows = (size_t)batch * seq, packed = rows * n_heads * 256;
+  const Span spans[] = {{o, packed}, {lse, rows * n_heads * 4}, {qp, packed}, {kp, packed}, {qkv, 3 * packed}, {key_mask, rows}};
+  if (any_overlap(spans, 2, 6)) return fail(MI_ERR_INVALID_ARG, "an output overlaps another tensor");
+  return attention_common(qp, kp, qkv, key_mask, o, lse, batch, seq, n_heads, ws, ws_bytes, ws != nullptr, stream);
+}
+
+namespace {
+
+int padded_seq(int seq) { return (seq + 127) / 128 * 128; }
+
+// Bytes of one of the two per-row arrays of the attention's gradient.
+size_t bwd_rows_bytes(int batch, int seq, int n_heads) {
+  return align_up((size_t)batch * n_heads * padded_seq(seq) * sizeof(float), 256);
+}
+
+}  // namespace
+
+mi_status mi_attention_backward_workspace_size(int batch, int seq, int n_heads, size_t* bytes) {
+  if (!bytes) return fail(MI_ERR_INVALID_ARG, "null output pointer");
+  mi_status st = check_train_shape(batch, seq, n_heads);
+  if (st != MI_OK) return st;
+  *bytes = 2 * bwd_rows_bytes(batch, seq, n_heads);
+  return MI_OK;
+}
+
+mi_status mi_attention_backward(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, const void* o,
+                                const float* lse, const void* d_o, void* dqp, void* dkp, void* dqkv, int batch, int seq,
+                                int n_heads, void* ws, size_t ws_bytes, void* stream) {
+  if (!qp || !kp || !qkv || !o || !lse || !d_o || !dqp || !dkp || !dqkv)
+    return fail(MI_ERR_INVALID_ARG, "null tensor argument");
+  if (!aligned16(qp) || !aligned16(kp) || !aligned16(qkv) || !aligned16(o) || !aligned16(lse) || !aligned16(d_o) ||
+      !aligned16(dqp) || !aligned16(dkp) || !aligned16(dqkv))
+    return fail(MI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  mi_status st = check_train_shape(batch, seq, n_heads);
+  if (st != MI_OK) return st;
+  const size_t rows_bytes = bwd_rows_bytes(batch, seq, n_heads);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(MI_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
+  if (ws_bytes < 2 * rows_bytes) return fail(MI_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, 2 * rows_bytes);
+  const size_t rows = (size_t)batch * seq, packed = rows * n_heads * 256;
+  const Span spans[] = {{dqp, packed}, {dkp, packed}, {dqkv, 3 * packed}, {ws, 2 * rows_bytes}, {qp, packed}, {kp, packed},
+                        {qkv, 3 * packed}, {o, packed}, {d_o, packed}, {lse, rows * n_heads * 4}, {key_mask, rows}};
+  if (any_overlap(spans, 4, 11)) return fail(MI_ERR_INVALID_ARG, "an output or the workspace overlaps another tensor");
+  DeviceInfo* dev = nullptr;
+  st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  const uint64_t H = (uint64_t)n_heads * 128, S = (uint64_t)seq;
+  CUtensorMap tq, tk, tv, tdo;
+  if (!mi::encode_3d_bf16(&tq, qp, 128, S, (uint64_t)batch * n_heads, 256, S * 256, 64, 128, 1) ||
+      !mi::encode_3d_bf16(&tk, kp, 128, S, (uint64_t)batch * n_heads, 256, S * 256, 64, 128, 1))
+    return fail(MI_ERR_INVALID_ARG, "tensor map encoding failed (q/k)");
+  const uint64_t dims[4] = {128, (uint64_t)n_heads, S, (uint64_t)batch};
+  const uint64_t v_str[3] = {256, 3 * H * 2, S * 3 * H * 2}, do_str[3] = {256, H * 2, S * H * 2};
+  const uint32_t box[4] = {64, 1, 128, 1};
+  if (!mi::encode_4d_bf16(&tv, cb(qkv) + 2 * H, dims, v_str, box) || !mi::encode_4d_bf16(&tdo, d_o, dims, do_str, box))
+    return fail(MI_ERR_INVALID_ARG, "tensor map encoding failed (v/d_o)");
+  mi::AttnBwdArgs a;
+  a.batch = batch;
+  a.seq = seq;
+  a.n_heads = n_heads;
+  a.seq_pad = padded_seq(seq);
+  a.key_mask = key_mask;
+  a.o = cb(o);
+  a.d_o = cb(d_o);
+  a.lse = lse;
+  a.lse2 = static_cast<float*>(ws);
+  a.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + rows_bytes);
+  a.dqp = mb(dqp);
+  a.dkp = mb(dkp);
+  a.dv = mb(dqkv) + 2 * H;
+  a.scale = 1.0f / sqrtf(128.0f);
+  a.scale_log2 = 1.4426950408889634f / sqrtf(128.0f);
+  a.err = dev->err;
+  cudaError_t e = mi::attention_bwd_launch(tq, tk, tv, tdo, a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MI_OK : cuda_fail(e, "attention backward launch");
+}
+
+mi_status mi_qk_norm_rope_backward_workspace_size(int batch, int seq, int n_heads, size_t* bytes) {
+  if (!bytes) return fail(MI_ERR_INVALID_ARG, "null output pointer");
+  mi_status st = check_train_shape(batch, seq, n_heads);
+  if (st != MI_OK) return st;
+  DeviceInfo* dev = nullptr;
+  st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  *bytes = (size_t)mi::qk_norm_rope_bwd_grid(batch, seq, n_heads, dev->num_sms) * 256 * sizeof(float);
+  return MI_OK;
+}
+
+mi_status mi_qk_norm_rope_backward(const void* qkv, const void* q_norm_w, const void* k_norm_w, const float* rope_cos,
+                                   const float* rope_sin, int rope_bstride, const void* dqp, const void* dkp, void* dqkv,
+                                   float* dq_norm_w, float* dk_norm_w, int batch, int seq, int n_heads, float eps,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  if (!qkv || !q_norm_w || !k_norm_w || !rope_cos || !rope_sin || !dqp || !dkp || !dqkv || !dq_norm_w || !dk_norm_w)
+    return fail(MI_ERR_INVALID_ARG, "null tensor argument");
+  if (!aligned16(qkv) || !aligned16(q_norm_w) || !aligned16(k_norm_w) || !aligned16(rope_cos) || !aligned16(rope_sin) ||
+      !aligned16(dqp) || !aligned16(dkp) || !aligned16(dqkv) || !aligned16(dq_norm_w) || !aligned16(dk_norm_w))
+    return fail(MI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  mi_status st = check_train_shape(batch, seq, n_heads);
+  if (st != MI_OK) return st;
+  if (rope_bstride < 0 || rope_bstride % 4 != 0) return fail(MI_ERR_INVALID_ARG, "bad rope_bstride");
+  if (!(eps >= 0.0f)) return fail(MI_ERR_INVALID_ARG, "eps must be >= 0");
+  DeviceInfo* dev = nullptr;
+  st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  const size_t need = (size_t)mi::qk_norm_rope_bwd_grid(batch, seq, n_heads, dev->num_sms) * 256 * sizeof(float);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(MI_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
+  if (ws_bytes < need) return fail(MI_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  const size_t packed = (size_t)batch * seq * n_heads * 256;
+  const size_t table = ((size_t)(batch - 1) * rope_bstride + (size_t)seq * 64) * 4;
+  const Span spans[] = {{dqkv, 3 * packed}, {dq_norm_w, 512}, {dk_norm_w, 512}, {ws, need}, {qkv, 3 * packed}, {dqp, packed},
+                        {dkp, packed}, {q_norm_w, 256}, {k_norm_w, 256}, {rope_cos, table}, {rope_sin, table}};
+  if (any_overlap(spans, 4, 11)) return fail(MI_ERR_INVALID_ARG, "an output or the workspace overlaps another tensor");
+  cudaError_t e = mi::qk_norm_rope_bwd_launch(cb(qkv), cb(q_norm_w), cb(k_norm_w), rope_cos, rope_sin, rope_bstride,
+                                              cb(dqp), cb(dkp), mb(dqkv), dq_norm_w, dk_norm_w, static_cast<float*>(ws),
+                                              batch, seq, n_heads, eps, dev->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MI_OK : cuda_fail(e, "qk_norm_rope backward");
 }
 
 mi_status mi_gated_add(const void* x, const void* y, const void* mod, int gate_row, void* out, int batch, int seq,
@@ -1063,6 +1221,35 @@ mi_status mi_rope_tables(int text_pad, int grid_h, int grid_w, float theta, floa
   cudaError_t e = mi::rope_table_launch(rope_cos, rope_sin, (int)S, text_pad, grid_w, (double)theta,
                                         static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MI_OK : cuda_fail(e, "rope tables");
+}
+
+mi_status mi_rope_axes_tables(const float* positions, int rows, int n_axes, const int* axis_pairs, float theta,
+                              float* rope_cos, float* rope_sin, void* stream) {
+  if (!positions || !axis_pairs || !rope_cos || !rope_sin) return fail(MI_ERR_INVALID_ARG, "null argument");
+  if (!aligned16(rope_cos) || !aligned16(rope_sin) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
+    return fail(MI_ERR_INVALID_ARG, "tables must be 16-byte aligned, positions 4-byte aligned");
+  if (rows <= 0 || rows > (1 << 28)) return fail(MI_ERR_INVALID_ARG, "rows=%d out of range", rows);
+  if (n_axes < 1 || n_axes > MI_ROPE_MAX_AXES) return fail(MI_ERR_INVALID_ARG, "n_axes=%d: 1..%d", n_axes, MI_ROPE_MAX_AXES);
+  if (!(theta > 1.0f) || !(theta < 3.0e38f)) return fail(MI_ERR_INVALID_ARG, "theta must be finite and above 1");
+  mi::RopeAxes f;
+  int at = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (axis_pairs[a] <= 0 || axis_pairs[a] > 64 - at)
+      return fail(MI_ERR_INVALID_ARG, "axis_pairs must be positive and add up to 64 (axis %d: %d)", a, axis_pairs[a]);
+    for (int j = 0; j < axis_pairs[a]; ++j, ++at) {
+      const double turns = pow((double)theta, -(double)j / axis_pairs[a]) / 6.283185307179586476925;
+      f.hi[at] = (float)turns;
+      f.lo[at] = (float)(turns - (double)f.hi[at]);
+      f.axis[at] = (unsigned char)a;
+    }
+  }
+  if (at != 64) return fail(MI_ERR_INVALID_ARG, "axis_pairs must be positive and add up to 64 (they give %d)", at);
+  DeviceInfo* dev = nullptr;
+  mi_status st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  cudaError_t e = mi::rope_axes_launch(positions, rows, n_axes, f, rope_cos, rope_sin, dev->num_sms,
+                                       static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MI_OK : cuda_fail(e, "rope axes tables");
 }
 
 mi_status mi_time_advance(float* t, int n, float dt, void* stream) {

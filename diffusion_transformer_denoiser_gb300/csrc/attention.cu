@@ -77,6 +77,11 @@ constexpr float kRescaleLog2 = 8.0f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
+// Natural-log log-sum-exp of a row from its reference max (base 2) and sum; -inf for an empty row.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : neg_inf();
+}
+
 constexpr int kPartRowFloats = 130;                     // a row's 128 O values, then m and l
 constexpr int kPartTileFloats = 128 * kPartRowFloats;   // one query tile of a part
 
@@ -104,6 +109,12 @@ __device__ int build_segments(int4* tab, long long total, int n_kv) {
 
 // 12 warps, 3 per SM sub-partition (16K registers each): 168 registers per thread at launch, which
 // the launch bound below lets the compiler derive; the roles then trade registers as above.
+//
+// kLse: the forward of a training pass.  It also stores each row's log-sum-exp, from which the gradient
+// recomputes the probabilities, and it clears the V rows of masked keys in shared memory (the wait
+// proxy does, which has V of each key tile before the MMA issuer may use it): their probabilities are
+// zero, but zero times an infinity or NaN in a padded row would not be.
+template <bool kLse>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const AttnArgs p) {
@@ -244,6 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               !mbar_wait_warp(&v_full[kt & 1], (uint32_t)((kt >> 1) & 1), abort_flag, p.err, DEV_TIMEOUT_ATTN + 9)) {
             ok = false;
             break;
+          }
+          if (kLse && p.key_mask != nullptr) {
+            const int4 sg = seg_tab[seg];
+            zero_masked_rows(sV + (kt & 1) * TILE_BYTES, p.key_mask + (size_t)(sg.x / n_qp / p.n_heads) * S,
+                             (sg.y + t) * BKV, S, lane);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[0]);
@@ -545,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (sg.y == 0 && sg.z == n_kv) {
         // the whole unit: normalise and store
         const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+        if (kLse && row < S) p.lse[(size_t)bh * S + row] = row_lse(m_run, l_run);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -601,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float wB = M == neg_inf() ? 0.0f : ex2_approx(mB - M);
           const float l = fmaf(wA, lA, wB * lB);
           const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+          if (kLse && row < S) p.lse[(size_t)bh * S + row] = row_lse(M, l);
           const float4* other4 = reinterpret_cast<const float4*>(other);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -651,25 +669,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t attention_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const AttnArgs& a, int num_sms, cudaStream_t s) {
+template <bool kLse>
+static cudaError_t attention_launch_as(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                       const AttnArgs& a, int num_sms, cudaStream_t s) {
   static bool attr_done[kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(attn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+    e = cudaFuncSetAttribute(attn_fwd_kernel<kLse>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
     if (e != cudaSuccess) return e;
     // the softmax warpgroups' register increase needs the pool the split was sized for
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, attn_fwd_kernel);
+    e = cudaFuncGetAttributes(&fa, attn_fwd_kernel<kLse>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs * kThreads < 128 * kRegsControl + 256 * kRegsSoftmax) return cudaErrorInvalidConfiguration;
     attr_done[dev] = true;
   }
-  return launch_kernel(attn_fwd_kernel, dim3(attention_grid(a.batch, a.seq, a.n_heads, a.part != nullptr ? num_sms : 0)),
+  return launch_kernel(attn_fwd_kernel<kLse>,
+                       dim3(attention_grid(a.batch, a.seq, a.n_heads, a.part != nullptr ? num_sms : 0)),
                        dim3(kThreads), SMEM_TOTAL, s, true, tq, tk, tv, a);
+}
+
+cudaError_t attention_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const AttnArgs& a, int num_sms, cudaStream_t s) {
+  return a.lse != nullptr ? attention_launch_as<true>(tq, tk, tv, a, num_sms, s)
+                          : attention_launch_as<false>(tq, tk, tv, a, num_sms, s);
 }
 
 // Units are split between CTAs (one per SM) only while there are at most 8 units per SM.  With

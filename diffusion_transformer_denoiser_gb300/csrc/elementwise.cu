@@ -277,6 +277,96 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __nv_bfloat16* 
   *reinterpret_cast<uint4*>(dst) = pack8(o);
 }
 
+// ------------------------------------------------------------------------------------ q/k gradient
+// With n = x r, r = rsqrt(mean x^2 + eps), y = rotate(n gain): the gradient of y is rotated back (dz),
+// dgain = sum of dz n over all rows and heads, and with t = dz gain, dx = r (t - n mean(t n)).
+// One warp per (row, head) as in the forward: lanes 0-15 q, lanes 16-31 k.  Each CTA sums its share of
+// dgain in registers and adds its warps' sums in a fixed order; a second kernel adds the CTAs' sums.
+constexpr int kQkBwdThreads = 256;
+
+__global__ void __launch_bounds__(kQkBwdThreads)
+    qk_norm_rope_bwd_kernel(const __nv_bfloat16* __restrict__ qkv, const __nv_bfloat16* __restrict__ wq,
+                            const __nv_bfloat16* __restrict__ wk, const float* __restrict__ cosv,
+                            const float* __restrict__ sinv, int rope_bstride, const __nv_bfloat16* __restrict__ dqp,
+                            const __nv_bfloat16* __restrict__ dkp, __nv_bfloat16* __restrict__ dqkv,
+                            float* __restrict__ partial, int batch, int seq, int heads, float eps) {
+  __shared__ float sums[kQkBwdThreads / 32][256];
+  grid_dep_wait();
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int which = lane >> 4;  // 0: q, 1: k
+  const int e0 = (lane & 15) * 8;
+  const int H = heads * kHeadDim;
+  const long long total = (long long)batch * seq * heads;
+  const long long stride = (long long)gridDim.x * (kQkBwdThreads / 32);
+  float g[8], dg[8];
+  unpack8(__ldg(reinterpret_cast<const uint4*>((which ? wk : wq) + e0)), g);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dg[e] = 0.0f;
+  for (long long item = (long long)blockIdx.x * (kQkBwdThreads / 32) + warp; item < total; item += stride) {
+    const int h = (int)(item % heads);
+    const long long row = item / heads;
+    const int b = (int)(row / seq);
+    const int s = (int)(row % seq);
+    const size_t at = (size_t)row * 3 * H + (size_t)which * H + (size_t)h * kHeadDim + e0;
+    const uint4 xv = *reinterpret_cast<const uint4*>(qkv + at);
+    const uint4 yv = *reinterpret_cast<const uint4*>((which ? dkp : dqp) + (((size_t)b * heads + h) * seq + s) * kHeadDim + e0);
+    const size_t tab = (size_t)b * rope_bstride + (size_t)s * (kHeadDim / 2) + (lane & 15) * 4;
+    const float4 c4 = __ldg(reinterpret_cast<const float4*>(cosv + tab));
+    const float4 s4 = __ldg(reinterpret_cast<const float4*>(sinv + tab));
+    const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+    float x[8], y[8];
+    unpack8(xv, x);
+    unpack8(yv, y);
+#pragma unroll
+    for (int pr = 0; pr < 4; ++pr) {
+      const float a = y[2 * pr], bb = y[2 * pr + 1];
+      y[2 * pr] = fmaf(a, cs[pr], bb * sn[pr]);
+      y[2 * pr + 1] = fmaf(bb, cs[pr], -a * sn[pr]);
+    }
+    float ss = 0.0f, tx = 0.0f;  // sums of x^2 and of t x
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      ss = fmaf(x[e], x[e], ss);
+      tx = fmaf(y[e] * g[e], x[e], tx);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      tx += __shfl_xor_sync(0xffffffffu, tx, o);
+    }
+    const float r = rsqrtf(ss * (1.0f / kHeadDim) + eps);
+    const float m = tx * r * r * (1.0f / kHeadDim);  // mean(t n) r
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dg[e] = fmaf(y[e], x[e] * r, dg[e]);
+      o[e] = r * fmaf(y[e], g[e], -x[e] * m);
+    }
+    *reinterpret_cast<uint4*>(dqkv + at) = pack8(o);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[warp][which * 128 + e0 + e] = dg[e];
+  __syncthreads();
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kQkBwdThreads / 32; ++w) t += sums[w][threadIdx.x];
+  partial[(size_t)blockIdx.x * 256 + threadIdx.x] = t;
+}
+
+// dgain[c] = sum of the CTAs' partial sums; four groups of threads take every fourth CTA each.
+__global__ void __launch_bounds__(1024) qk_gain_sum_kernel(const float* __restrict__ partial, int n,
+                                                           float* __restrict__ dwq, float* __restrict__ dwk) {
+  __shared__ float sums[4][256];
+  grid_dep_wait();
+  const int c = threadIdx.x & 255, grp = threadIdx.x >> 8;
+  float t = 0.0f;
+  for (int i = grp; i < n; i += 4) t += partial[(size_t)i * 256 + c];
+  sums[grp][c] = t;
+  __syncthreads();
+  if (grp == 0) (c < 128 ? dwq : dwk)[c & 127] = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+}
+
 // ------------------------------------------------------------------------------------ gated add
 // out = x + gate[b] * y (fp32 fma, one rounding); the same expression as the fused GEMM epilogue.
 __global__ void __launch_bounds__(256) gated_add_kernel(const __nv_bfloat16* __restrict__ x,
@@ -384,6 +474,46 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* __restrict__ cos
   sinv[i] = (float)sin(ang);
 }
 
+// Rotary tables from per-token positions: pair j of row r turns by pos[r, axis j] (hi_j + lo_j) full
+// turns, hi + lo a frequency over 2 pi in 48 bits.  The product is formed in fp32 pairs (its rounding
+// recovered by one fma), whole quarter turns are taken off exactly, and the sine and cosine see at
+// most an eighth of a turn: the angle is as exact as in 64 bits up to positions of 2^24.  16 lanes take
+// a row, 4 pairs each, and keep their frequencies in registers over the rows of a grid-stride loop.
+__global__ void __launch_bounds__(256) rope_axes_kernel(const float* __restrict__ pos, int rows, int n_axes,
+                                                        const __grid_constant__ RopeAxes f, float* __restrict__ cosv,
+                                                        float* __restrict__ sinv) {
+  grid_dep_wait();
+  const int j0 = (threadIdx.x & 15) * 4;
+  float hi[4], lo[4];
+  int axis[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = f.hi[j0 + i];
+    lo[i] = f.lo[j0 + i];
+    axis[i] = f.axis[j0 + i];
+  }
+  const int stride = gridDim.x * 16;
+  for (long long r = blockIdx.x * 16 + (threadIdx.x >> 4); r < rows; r += stride) {
+    float c[4], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p = __ldg(pos + r * n_axes + axis[i]);
+      const float t = p * hi[i];
+      const float rest = fmaf(p, lo[i], fmaf(p, hi[i], -t));
+      const float n = rintf(4.0f * t);
+      const float turn = fmaf(n, -0.25f, t) + rest;
+      const int quarter = (int)(n - 4.0f * floorf(0.25f * n));
+      float sv, cv;
+      sincospif(2.0f * turn, &sv, &cv);
+      const float cq = (quarter & 1) ? sv : cv, sq = (quarter & 1) ? cv : sv;
+      c[i] = (quarter == 1 || quarter == 2) ? -cq : cq;
+      s[i] = (quarter >= 2) ? -sq : sq;
+    }
+    *reinterpret_cast<float4*>(cosv + r * 64 + j0) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4*>(sinv + r * 64 + j0) = make_float4(s[0], s[1], s[2], s[3]);
+  }
+}
+
 // Sinusoidal timestep embedding: out[b, k] = cos(scale t_b f_k), out[b, half + k] = sin(scale t_b f_k),
 // f_k = max_period^(-k / half); fp64, rounded to bf16.
 __global__ void __launch_bounds__(256) timestep_embedding_kernel(const float* __restrict__ t, __nv_bfloat16* __restrict__ out,
@@ -471,6 +601,24 @@ cudaError_t qk_norm_rope_launch(const __nv_bfloat16* qkv, const __nv_bfloat16* w
   return cudaGetLastError();
 }
 
+int qk_norm_rope_bwd_grid(int batch, int seq, int n_heads, int num_sms) {
+  const long long need = ((long long)batch * seq * n_heads + kQkBwdThreads / 32 - 1) / (kQkBwdThreads / 32);
+  const long long cap = 4LL * num_sms;
+  return (int)(need < cap ? need : cap);
+}
+
+cudaError_t qk_norm_rope_bwd_launch(const __nv_bfloat16* qkv, const __nv_bfloat16* wq, const __nv_bfloat16* wk,
+                                    const float* cos, const float* sin, int rope_bstride, const __nv_bfloat16* dqp,
+                                    const __nv_bfloat16* dkp, __nv_bfloat16* dqkv, float* dwq, float* dwk,
+                                    float* partial, int batch, int seq, int n_heads, float eps, int num_sms,
+                                    cudaStream_t s) {
+  const int grid = qk_norm_rope_bwd_grid(batch, seq, n_heads, num_sms);
+  cudaError_t e = launch_kernel(qk_norm_rope_bwd_kernel, dim3(grid), dim3(kQkBwdThreads), 0, s, true, qkv, wq, wk, cos, sin,
+                                rope_bstride, dqp, dkp, dqkv, partial, batch, seq, n_heads, eps);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(qk_gain_sum_kernel, dim3(1), dim3(1024), 0, s, true, (const float*)partial, grid, dwq, dwk);
+}
+
 cudaError_t gated_add_launch(const __nv_bfloat16* x, const __nv_bfloat16* y, const __nv_bfloat16* gate,
                              int gate_bstride, __nv_bfloat16* out, int rows, int seq, int hidden, cudaStream_t s) {
   const long long n_vec = (long long)rows * hidden / 8;
@@ -517,6 +665,14 @@ cudaError_t rope_table_launch(float* cosv, float* sinv, int S, int text_pad, int
   if (S <= 0) return cudaSuccess;
   rope_table_kernel<<<(S * 64 + 255) / 256, 256, 0, s>>>(cosv, sinv, S, text_pad, grid_w, theta);
   return cudaGetLastError();
+}
+
+cudaError_t rope_axes_launch(const float* pos, int rows, int n_axes, const RopeAxes& f, float* cosv, float* sinv,
+                             int num_sms, cudaStream_t s) {
+  const int need = (rows + 15) / 16;
+  const int cap = 8 * num_sms;
+  return launch_kernel(rope_axes_kernel, dim3(need < cap ? need : cap), dim3(256), 0, s, true, pos, rows, n_axes, f, cosv,
+                       sinv);
 }
 
 cudaError_t timestep_embedding_launch(const float* t, __nv_bfloat16* out, int batch, int dim, double scale,

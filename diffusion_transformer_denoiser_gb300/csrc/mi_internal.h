@@ -68,6 +68,7 @@ struct AttnArgs {
   // per SM and units may be split between neighbouring CTAs; without it, one CTA per unit.
   float* part;                 // partial results of split units, two slots per CTA
   int* count;                  // [units][2] arrival counters, zero at launch (left zero after it)
+  float* lse;                  // [B, n_heads, S] log-sum-exp of each row's scaled scores, or null
 };
 
 // q/k maps: 3-D over (128, S, B * n_heads); v map: 4-D over (128, n_heads, S, B) of the qkv buffer.
@@ -79,6 +80,45 @@ int attention_grid(int batch, int seq, int n_heads, int num_sms);
 // its arrival counters, which come first.
 size_t attention_scratch_bytes(int batch, int seq, int n_heads, int num_sms);
 size_t attention_count_bytes(int batch, int seq, int n_heads);
+
+// Gradient of the attention (attention_bwd.cu).
+struct AttnBwdArgs {
+  int batch, seq, n_heads;
+  int seq_pad;                 // seq rounded up to whole 128-row tiles: the row length of lse2 and delta
+  const uint8_t* key_mask;     // [B, S] or null
+  const __nv_bfloat16* o;      // [B, S, n_heads * 128], as the forward wrote it
+  const __nv_bfloat16* d_o;    // [B, S, n_heads * 128]
+  const float* lse;            // [B, n_heads, S]
+  float* lse2;                 // [B * n_heads, seq_pad]: lse in base 2, +inf for an empty or missing row
+  float* delta;                // [B * n_heads, seq_pad]: sum_d d_o o of the row
+  __nv_bfloat16* dqp;          // [B, n_heads, S, 128]
+  __nv_bfloat16* dkp;
+  __nv_bfloat16* dv;           // v columns of row 0 of dqkv; rows 3 * n_heads * 128 apart
+  float scale;                 // 1 / sqrt(128)
+  float scale_log2;            // log2(e) / sqrt(128)
+  int* err;
+};
+
+// q, k maps as for the forward; v: 4-D over (128, n_heads, S, B) of the qkv buffer; d_o: the same over d_o.
+cudaError_t attention_bwd_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const CUtensorMap& tdo, const AttnBwdArgs& a, cudaStream_t s);
+
+// Gradient of the q/k RMSNorm + rotary (elementwise.cu).  partial: [qk_norm_rope_bwd_grid()][256] floats.
+cudaError_t qk_norm_rope_bwd_launch(const __nv_bfloat16* qkv, const __nv_bfloat16* wq, const __nv_bfloat16* wk,
+                                    const float* cos, const float* sin, int rope_bstride, const __nv_bfloat16* dqp,
+                                    const __nv_bfloat16* dkp, __nv_bfloat16* dqkv, float* dwq, float* dwk,
+                                    float* partial, int batch, int seq, int n_heads, float eps, int num_sms,
+                                    cudaStream_t s);
+int qk_norm_rope_bwd_grid(int batch, int seq, int n_heads, int num_sms);
+
+// Rotary tables of tokens with several position axes (elementwise.cu): pair j of a row turns by
+// pos[row, axis[j]] * (hi[j] + lo[j]) full turns.
+struct RopeAxes {
+  float hi[64], lo[64];
+  unsigned char axis[64];
+};
+cudaError_t rope_axes_launch(const float* pos, int rows, int n_axes, const RopeAxes& f, float* cosv, float* sinv,
+                             int num_sms, cudaStream_t s);
 
 // Element-wise kernels (elementwise.cu).
 // zero/zero_n: an int array the kernel clears (after the previous kernel in the stream is done),

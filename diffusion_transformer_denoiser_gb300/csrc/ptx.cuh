@@ -21,6 +21,7 @@ enum : int {
   DEV_TIMEOUT_SELFTEST = 0x300,
   DEV_SCHEDULE_GEMM = 0x400,  // a GEMM launch whose stream-K plan the kernel cannot carry out
   DEV_TIMEOUT_NORM = 0x500,
+  DEV_TIMEOUT_ATTN_BWD = 0x600,
 };
 
 // Polls of a single wait.  A poll (mbarrier.try_wait) that finds the phase incomplete suspends the
@@ -187,6 +188,27 @@ __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol
 // Make this thread's generic-proxy shared-memory writes visible to the async proxy (UMMA, TMA).
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Clears the rows of masked keys in a 128-key x 128 bf16 tile (two 128-byte-swizzled halves of 16 KB:
+// a row is 128 contiguous bytes of each half, whatever its swizzle).  mask: the key mask of the batch
+// element, k0: first key of the tile, seq: keys of the element (the copy has zero-filled those past
+// it).  Called by a whole warp once the tile has landed; ordered before later MMAs of the tile.
+__device__ __forceinline__ void zero_masked_rows(uint8_t* tile, const uint8_t* mask, int k0, int seq, int lane) {
+  bool touched = false;
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w) {
+    const int kc = k0 + w * 32 + lane;
+    uint32_t bad = __ballot_sync(0xffffffffu, kc < seq && mask[kc < seq ? kc : 0] == 0);
+    while (bad != 0) {
+      const int row = w * 32 + __ffs(bad) - 1;
+      bad &= bad - 1;
+      if (lane < 16)
+        *reinterpret_cast<uint4*>(tile + (lane >> 3) * 16384 + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+      touched = true;
+    }
+  }
+  if (touched) fence_proxy_async_smem();
 }
 
 // ------------------------------------------------------------------------------------ tcgen05

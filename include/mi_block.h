@@ -66,12 +66,13 @@ mi_status mi_device_error(int* code);
 /* Error codes mi_device_error reports: 0x100 + k (a GEMM wait), 0x200 + k (an attention wait),
  * 0x300 (the self-test below), 0x400 (a GEMM whose split of tail tiles over the CTAs has more parts
  * per tile than its fix-up adds; the library's own plans never produce one), 0x500 + k (a wait of
- * the modulated RMSNorm for its row copies). */
+ * the modulated RMSNorm for its row copies), 0x600 + k (a wait of the attention's gradient). */
 #define MI_DEV_TIMEOUT_GEMM 0x100
 #define MI_DEV_TIMEOUT_ATTN 0x200
 #define MI_DEV_TIMEOUT_SELFTEST 0x300
 #define MI_DEV_SCHEDULE_GEMM 0x400
 #define MI_DEV_TIMEOUT_NORM 0x500
+#define MI_DEV_TIMEOUT_ATTN_BWD 0x600
 
 /* Enqueues a one-CTA kernel whose pipeline wait can never complete: the wait gives up after about
  * limit_us microseconds (at most 1e6; the pipelines' own bounded wait, given as many polls as take
@@ -252,6 +253,19 @@ mi_status mi_denoise_step(mi_model* model, const mi_seq_layout* L, void* latent,
 mi_status mi_rope_tables(int text_pad, int grid_h, int grid_w, float theta, float* rope_cos, float* rope_sin,
                          void* stream);
 
+/* Rotary tables of tokens with several position axes (time, row, column of a video token, for
+ * example), fp32 [rows, 64]: axis a has axis_pairs[a] consecutive pairs, and its pair j of row r turns by
+ * positions[r, a] * theta^(-j / axis_pairs[a]).  With axis_pairs {32, 32} and (row, column) positions
+ * these are the tables of mi_rope_tables.  rows = S for tables shared by a batch (rope_bstride 0 in the
+ * calls that read them), batch * S for tables of each element (rope_bstride = 64 S).
+ *   positions   device fp32 [rows, n_axes], whole or not, of either sign; up to |position| = 2^24 the
+ *               tables are within 3 * 2^-24 of the 64-bit values (a position that is not finite gives NaN)
+ *   n_axes      1..MI_ROPE_MAX_AXES
+ *   axis_pairs  HOST array of n_axes positive counts that add up to 64 */
+#define MI_ROPE_MAX_AXES 8
+mi_status mi_rope_axes_tables(const float* positions, int rows, int n_axes, const int* axis_pairs, float theta,
+                              float* rope_cos, float* rope_sin, void* stream);
+
 typedef struct mi_tmod_desc {
   int hidden;          /* H, multiple of 256 */
   int n_blocks;
@@ -342,6 +356,45 @@ mi_status mi_attention(const void* qp, const void* kp, const void* qkv, const ui
 mi_status mi_attention_workspace_size(int batch, int seq, int n_heads, size_t* bytes);
 mi_status mi_attention_ws(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, void* o,
                           int batch, int seq, int n_heads, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------- training pass --- */
+/* The attention section's forward and gradient: mi_qk_norm_rope (or tables from
+ * mi_rope_axes_tables), mi_attention_lse, and backwards mi_attention_backward, then
+ * mi_qk_norm_rope_backward.  The two backward calls fill disjoint columns of one dqkv
+ * [batch * seq, 3H], which is then the gradient of the whole QKV projection's output.  The projection
+ * must have stored all of qkv (mi_gemm_bf16, not mi_gemm_bf16_qkv_rope, which leaves out the q and k
+ * columns).  batch * seq * n_heads is at most 2^30, seq at most 2^20. */
+
+/* mi_attention that also stores lse fp32 [batch, heads, seq], the natural logarithm of
+ * sum_j exp(q_i k_j / sqrt(128)) over the valid keys (-inf for a row without one, whose output is zero).
+ * A masked key's rows of kp and v may hold anything, infinities and NaN included; every row of qp is a
+ * query and counts.
+ * ws: mi_attention_workspace_size bytes, 256-byte aligned, for the split schedule of mi_attention_ws, or
+ * NULL for one CTA per query-tile pair. */
+mi_status mi_attention_lse(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, void* o, float* lse,
+                           int batch, int seq, int n_heads, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of mi_attention_lse for the output gradient d_o [batch * seq, heads * 128]: dqp, dkp
+ * [batch, heads, seq, 128], and dv in columns [2H, 3H) of dqkv [batch * seq, 3H] (its other columns are
+ * not written).  o and lse are the forward's; the probabilities are recomputed from lse, so nothing of
+ * size seq^2 is stored.  Masked keys get zero gradients, and so do rows without a valid key.  Outputs
+ * that overlap an input or each other are refused.  ws: mi_attention_backward_workspace_size bytes,
+ * 256-byte aligned; it holds nothing between calls. */
+mi_status mi_attention_backward_workspace_size(int batch, int seq, int n_heads, size_t* bytes);
+mi_status mi_attention_backward(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, const void* o,
+                                const float* lse, const void* d_o, void* dqp, void* dkp, void* dqkv, int batch, int seq,
+                                int n_heads, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of mi_qk_norm_rope: from dqp, dkp [batch, heads, seq, 128] and the forward's inputs, the q and
+ * k columns [0, 2H) of dqkv [batch * seq, 3H] (the v columns are not written) and the gradients of the two
+ * gains, dq_norm_w and dk_norm_w, fp32 [128], summed over batch, rows and heads in a fixed order
+ * (overwritten, not added to).  Outputs that overlap an input or each other are refused.  ws:
+ * mi_qk_norm_rope_backward_workspace_size bytes, 256-byte aligned; it holds nothing between calls. */
+mi_status mi_qk_norm_rope_backward_workspace_size(int batch, int seq, int n_heads, size_t* bytes);
+mi_status mi_qk_norm_rope_backward(const void* qkv, const void* q_norm_w, const void* k_norm_w, const float* rope_cos,
+                                   const float* rope_sin, int rope_bstride, const void* dqp, const void* dkp, void* dqkv,
+                                   float* dq_norm_w, float* dk_norm_w, int batch, int seq, int n_heads, float eps,
+                                   void* ws, size_t ws_bytes, void* stream);
 
 /* out = x + mod[b, gate_row] * y, b = row / seq; x, y, out [batch * seq, hidden].  PR #1528,
  * "What it adds" (the gated add kernel; fp32 arithmetic, one bf16 rounding).  out may equal x. */
