@@ -973,8 +973,8 @@ mi_status mi_attention_backward(const void* qp, const void* kp, const void* qkv,
   a.o = cb(o);
   a.d_o = cb(d_o);
   a.lse = lse;
-  a.lse2 = static_cast<float*>(ws);
-  a.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + rows_bytes);
+  a.nlse2 = static_cast<float*>(ws);
+  a.ndelta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + rows_bytes);
   a.dqp = mb(dqp);
   a.dkp = mb(dkp);
   a.dv = mb(dqkv) + 2 * H;

@@ -251,16 +251,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // each arrival belongs to the phase of key tile kt: the previous phase of the barrier
           // must be complete first (the copies often land a key tile ahead of the softmax)
           const uint32_t prev = (uint32_t)((kt - 1) & 1);
+          uint32_t bad[4] = {0, 0, 0, 0};
+          if (kLse && p.key_mask != nullptr) {
+            const int4 sg = seg_tab[seg];
+            masked_keys(p.key_mask + (size_t)(sg.x / n_qp / p.n_heads) * S, (sg.y + t) * BKV, S, lane, bad);
+          }
           if ((kt > 0 && !mbar_wait_warp(&p_full[0], prev, abort_flag, p.err, DEV_TIMEOUT_ATTN + 9)) ||
               !mbar_wait_warp(&v_full[kt & 1], (uint32_t)((kt >> 1) & 1), abort_flag, p.err, DEV_TIMEOUT_ATTN + 9)) {
             ok = false;
             break;
           }
-          if (kLse && p.key_mask != nullptr) {
-            const int4 sg = seg_tab[seg];
-            zero_masked_rows(sV + (kt & 1) * TILE_BYTES, p.key_mask + (size_t)(sg.x / n_qp / p.n_heads) * S,
-                             (sg.y + t) * BKV, S, lane);
-          }
+          if (kLse) zero_rows(sV + (kt & 1) * TILE_BYTES, bad, lane);
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[0]);
           if ((kt > 0 && !mbar_wait_warp(&p_full[1], prev, abort_flag, p.err, DEV_TIMEOUT_ATTN + 9)) ||

@@ -28,12 +28,6 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 __device__ __forceinline__ float silu_f(float g) { return g / (1.0f + __expf(-g)); }
 
-__device__ __forceinline__ f32x2_t f2_mul(f32x2_t a, f32x2_t b) {
-  f32x2_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // ------------------------------------------------------------------------------------ adaLN norm
 // out[i] = x[in_row(i)] * rsqrt(mean(x^2) + eps) * (1 + scale[b]) + shift[b]; one warp per row.
 // Row i of the output reads input row (i / out_seq) * in_seq + in_off + i % out_seq, which lets

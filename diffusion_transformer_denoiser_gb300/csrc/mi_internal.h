@@ -84,13 +84,13 @@ size_t attention_count_bytes(int batch, int seq, int n_heads);
 // Gradient of the attention (attention_bwd.cu).
 struct AttnBwdArgs {
   int batch, seq, n_heads;
-  int seq_pad;                 // seq rounded up to whole 128-row tiles: the row length of lse2 and delta
+  int seq_pad;                 // seq rounded up to whole 128-row tiles: the row length of nlse2 and ndelta
   const uint8_t* key_mask;     // [B, S] or null
   const __nv_bfloat16* o;      // [B, S, n_heads * 128], as the forward wrote it
   const __nv_bfloat16* d_o;    // [B, S, n_heads * 128]
   const float* lse;            // [B, n_heads, S]
-  float* lse2;                 // [B * n_heads, seq_pad]: lse in base 2, +inf for an empty or missing row
-  float* delta;                // [B * n_heads, seq_pad]: sum_d d_o o of the row
+  float* nlse2;                // [B * n_heads, seq_pad]: -lse in base 2, -inf for an empty or missing row
+  float* ndelta;               // [B * n_heads, seq_pad]: -sum_d d_o o of the row
   __nv_bfloat16* dqp;          // [B, n_heads, S, 128]
   __nv_bfloat16* dkp;
   __nv_bfloat16* dv;           // v columns of row 0 of dqkv; rows 3 * n_heads * 128 apart

@@ -190,25 +190,37 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Clears the rows of masked keys in a 128-key x 128 bf16 tile (two 128-byte-swizzled halves of 16 KB:
-// a row is 128 contiguous bytes of each half, whatever its swizzle).  mask: the key mask of the batch
-// element, k0: first key of the tile, seq: keys of the element (the copy has zero-filled those past
-// it).  Called by a whole warp once the tile has landed; ordered before later MMAs of the tile.
-__device__ __forceinline__ void zero_masked_rows(uint8_t* tile, const uint8_t* mask, int k0, int seq, int lane) {
-  bool touched = false;
-#pragma unroll 1
+// Masked keys of a 128-key tile from key k0 on, as bits: word w holds keys k0 + 32 w .. (keys past seq
+// are not among them: the copy has zero-filled their rows).  Called by a whole warp.
+__device__ __forceinline__ void masked_keys(const uint8_t* mask, int k0, int seq, int lane, uint32_t (&bad)[4]) {
+  bool b[4];
+#pragma unroll
   for (int w = 0; w < 4; ++w) {
     const int kc = k0 + w * 32 + lane;
-    uint32_t bad = __ballot_sync(0xffffffffu, kc < seq && mask[kc < seq ? kc : 0] == 0);
-    while (bad != 0) {
-      const int row = w * 32 + __ffs(bad) - 1;
-      bad &= bad - 1;
-      if (lane < 16)
-        *reinterpret_cast<uint4*>(tile + (lane >> 3) * 16384 + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-      touched = true;
+    b[w] = kc < seq && mask[kc < seq ? kc : 0] == 0;
+  }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) bad[w] = __ballot_sync(0xffffffffu, b[w]);
+}
+
+// Clears those rows of a 128 x 128 bf16 tile (two 128-byte-swizzled halves of 16 KB: a row is 128
+// contiguous bytes of each half, whatever its swizzle), once the tile has landed; lanes 0-15 take one
+// row, lanes 16-31 the next.  Ordered before later MMAs of the tile.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, const uint32_t (&bad)[4], int lane) {
+  if ((bad[0] | bad[1] | bad[2] | bad[3]) == 0) return;
+  uint8_t* at = tile + ((lane >> 3) & 1) * 16384 + (lane & 7) * 16;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t m = bad[w];
+    while (m != 0) {
+      const int first = __ffs(m) - 1;
+      m &= m - 1;
+      const int second = m != 0 ? __ffs(m) - 1 : first;
+      m &= m - 1;
+      *reinterpret_cast<uint4*>(at + (w * 32 + (lane < 16 ? first : second)) * 128) = make_uint4(0, 0, 0, 0);
     }
   }
-  if (touched) fence_proxy_async_smem();
+  fence_proxy_async_smem();
 }
 
 // ------------------------------------------------------------------------------------ tcgen05
@@ -467,6 +479,12 @@ __device__ __forceinline__ f32x2_t f2_fma(f32x2_t a, f32x2_t b, f32x2_t c) {
 __device__ __forceinline__ f32x2_t f2_add(f32x2_t a, f32x2_t b) {
   f32x2_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ f32x2_t f2_mul(f32x2_t a, f32x2_t b) {
+  f32x2_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
