@@ -970,6 +970,7 @@ mi_status mi_attention_backward(const void* qp, const void* kp, const void* qkv,
   a.n_heads = n_heads;
   a.seq_pad = padded_seq(seq);
   a.key_mask = key_mask;
+  a.qp = cb(qp);
   a.o = cb(o);
   a.d_o = cb(d_o);
   a.lse = lse;

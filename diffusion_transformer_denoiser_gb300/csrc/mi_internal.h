@@ -86,6 +86,7 @@ struct AttnBwdArgs {
   int batch, seq, n_heads;
   int seq_pad;                 // seq rounded up to whole 128-row tiles: the row length of nlse2 and ndelta
   const uint8_t* key_mask;     // [B, S] or null
+  const __nv_bfloat16* qp;     // [B, n_heads, S, 128]
   const __nv_bfloat16* o;      // [B, S, n_heads * 128], as the forward wrote it
   const __nv_bfloat16* d_o;    // [B, S, n_heads * 128]
   const float* lse;            // [B, n_heads, S]
