@@ -916,11 +916,12 @@ mi_status mi_attention_lse(const void* qp, const void* kp, const void* qkv, cons
 
 namespace {
 
-int padded_seq(int seq) { return (seq + 127) / 128 * 128; }
-
-// Bytes of one of the two per-row arrays of the attention's gradient.
-size_t bwd_rows_bytes(int batch, int seq, int n_heads) {
-  return align_up((size_t)batch * n_heads * padded_seq(seq) * sizeof(float), 256);
+// The shape's part of the arguments, and the workspace's bytes.
+size_t plan_attention_backward(mi::AttnBwdArgs* a, int batch, int seq, int n_heads, void* ws) {
+  a->batch = batch;
+  a->seq = seq;
+  a->n_heads = n_heads;
+  return mi::attention_bwd_plan(a, static_cast<uint8_t*>(ws));
 }
 
 }  // namespace
@@ -929,7 +930,8 @@ mi_status mi_attention_backward_workspace_size(int batch, int seq, int n_heads, 
   if (!bytes) return fail(MI_ERR_INVALID_ARG, "null output pointer");
   mi_status st = check_train_shape(batch, seq, n_heads);
   if (st != MI_OK) return st;
-  *bytes = 2 * bwd_rows_bytes(batch, seq, n_heads);
+  mi::AttnBwdArgs a;
+  *bytes = plan_attention_backward(&a, batch, seq, n_heads, nullptr);
   return MI_OK;
 }
 
@@ -943,46 +945,42 @@ mi_status mi_attention_backward(const void* qp, const void* kp, const void* qkv,
     return fail(MI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
   mi_status st = check_train_shape(batch, seq, n_heads);
   if (st != MI_OK) return st;
-  const size_t rows_bytes = bwd_rows_bytes(batch, seq, n_heads);
+  mi::AttnBwdArgs a;
+  const size_t need = plan_attention_backward(&a, batch, seq, n_heads, ws);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return fail(MI_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
-  if (ws_bytes < 2 * rows_bytes) return fail(MI_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, 2 * rows_bytes);
+  if (ws_bytes < need) return fail(MI_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
   const size_t rows = (size_t)batch * seq, packed = rows * n_heads * 256;
-  const Span spans[] = {{dqp, packed}, {dkp, packed}, {dqkv, 3 * packed}, {ws, 2 * rows_bytes}, {qp, packed}, {kp, packed},
+  const Span spans[] = {{dqp, packed}, {dkp, packed}, {dqkv, 3 * packed}, {ws, need}, {qp, packed}, {kp, packed},
                         {qkv, 3 * packed}, {o, packed}, {d_o, packed}, {lse, rows * n_heads * 4}, {key_mask, rows}};
   if (any_overlap(spans, 4, 11)) return fail(MI_ERR_INVALID_ARG, "an output or the workspace overlaps another tensor");
   DeviceInfo* dev = nullptr;
   st = require_sm103(&dev);
   if (st != MI_OK) return st;
   const uint64_t H = (uint64_t)n_heads * 128, S = (uint64_t)seq;
-  CUtensorMap tq, tk, tv, tdo;
-  if (!mi::encode_3d_bf16(&tq, qp, 128, S, (uint64_t)batch * n_heads, 256, S * 256, 64, 128, 1) ||
-      !mi::encode_3d_bf16(&tk, kp, 128, S, (uint64_t)batch * n_heads, 256, S * 256, 64, 128, 1))
+  const uint64_t BH = (uint64_t)batch * n_heads;
+  mi::AttnBwdMaps m;
+  if (!mi::encode_3d_bf16(&m.q, qp, 128, S, BH, 256, S * 256, 64, 128, 1) ||
+      !mi::encode_3d_bf16(&m.k, kp, 128, S, BH, 256, S * 256, 64, 128, 1) ||
+      !mi::encode_3d_bf16(&m.dq, dqp, 128, S, BH, 256, S * 256, 64, 32, 1))
     return fail(MI_ERR_INVALID_ARG, "tensor map encoding failed (q/k)");
   const uint64_t dims[4] = {128, (uint64_t)n_heads, S, (uint64_t)batch};
   const uint64_t v_str[3] = {256, 3 * H * 2, S * 3 * H * 2}, do_str[3] = {256, H * 2, S * H * 2};
   const uint32_t box[4] = {64, 1, 128, 1};
-  if (!mi::encode_4d_bf16(&tv, cb(qkv) + 2 * H, dims, v_str, box) || !mi::encode_4d_bf16(&tdo, d_o, dims, do_str, box))
+  if (!mi::encode_4d_bf16(&m.v, cb(qkv) + 2 * H, dims, v_str, box) || !mi::encode_4d_bf16(&m.d_o, d_o, dims, do_str, box))
     return fail(MI_ERR_INVALID_ARG, "tensor map encoding failed (v/d_o)");
-  mi::AttnBwdArgs a;
-  a.batch = batch;
-  a.seq = seq;
-  a.n_heads = n_heads;
-  a.seq_pad = padded_seq(seq);
   a.key_mask = key_mask;
   a.qp = cb(qp);
   a.o = cb(o);
   a.d_o = cb(d_o);
   a.lse = lse;
-  a.nlse2 = static_cast<float*>(ws);
-  a.ndelta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + rows_bytes);
   a.dqp = mb(dqp);
   a.dkp = mb(dkp);
   a.dv = mb(dqkv) + 2 * H;
   a.scale = 1.0f / sqrtf(128.0f);
   a.scale_log2 = 1.4426950408889634f / sqrtf(128.0f);
   a.err = dev->err;
-  cudaError_t e = mi::attention_bwd_launch(tq, tk, tv, tdo, a, static_cast<cudaStream_t>(stream));
+  cudaError_t e = mi::attention_bwd_launch(m, a, dev->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MI_OK : cuda_fail(e, "attention backward launch");
 }
 

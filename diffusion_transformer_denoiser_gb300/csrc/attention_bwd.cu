@@ -9,14 +9,19 @@
 // (Q, dO) and walks the key tiles: S, dP, dQ += dS K.  That is 7 products of 128 x 128 x 128 per pair of
 // tiles where 5 are needed; the alternative, one pass that adds dQ tiles into memory, either gives up
 // the fixed order or makes CTAs wait for one another, and moves 64 KB of fp32 sums per pair of tiles.
-// One launch runs both: the CTAs of the keys pass come first, those of the (shorter) queries pass fill
-// the SMs as they free up.
+// One persistent launch runs both: a CTA takes units (a tile of one head) of the keys pass until there are
+// none, then units of the (shorter) queries pass.  The first unit follows from the CTA's index, the others
+// come from a counter in the workspace; which CTA computes a unit does not change its result.  The tiles
+// of successive units form one stream: while the last tile of a unit is worked on, the next unit's own
+// tiles land and its first scores are computed, and its first P (keys) or dS (queries) is withheld until
+// the accumulators of the unit before have been read out.
 //
 // In both passes a TMEM lane is a row of the tile the CTA holds, so P^T and dS^T (keys) or dS (queries)
 // go back to TMEM as bf16 and are the A operand of the product that sums over the streamed rows; the
 // streamed tiles serve both as the row-major operand of S and dP and, read along the other axis, as the
 // B operand of the sums.  Roles (384 threads, one CTA per SM):
-//   * warp 0: TMA producer: the CTA's own tiles, then the streamed tiles in rings of 2 or 3 stages.
+//   * warp 0: takes the units (one whose keys are all masked gets its zeros here and is left out) and is
+//     the TMA producer: the CTA's own tiles, the streamed tiles in rings of 2 or 3 stages.
 //   * warp 1: issues the MMAs (convergent warp, one elected lane per instruction).
 //       keys:    dV_n, S_{n+1} | dK_n, dP_{n+1}, each pair behind one wait: P_n (over S_n) and dS_n (over
 //                dP_n) are in the columns that the next scores overwrite, and the MMAs of one thread
@@ -27,7 +32,8 @@
 //   * warp 2: wait proxy: adds an arrival to the barriers above once the tile that the next product
 //     streams has landed, so that the issuer waits once per pair of products; it also clears masked K
 //     rows (queries pass): zero times an infinity or NaN in a padded row would not be zero.
-//   * warps 4-11: two warpgroups, each half of the 128 streamed rows; one thread per lane.
+//   * warps 4-11: two warpgroups, each half of the 128 streamed rows; one thread per lane.  They also read
+//     the accumulators out (queries pass: through shared memory, stored by TMA, a warp its own 32 rows).
 // P and dS are rounded to bf16 once, as matrix operands; scores, D, sums and P in dS are fp32.
 #include "mi_internal.h"
 #include "ptx.cuh"
@@ -47,17 +53,20 @@ constexpr int TILE_BYTES = BT * kHeadDim * 2;
 constexpr int HALF_BYTES = TILE_BYTES / 2;
 constexpr int STAT_BYTES = 2 * BT * 4;     // -lse2 and -delta of 128 queries
 
-// Shared memory: seven tiles, keys pass K | V | Q ring of 3 | dO ring of 2 and the row statistics with it;
-// queries pass dO | K ring of 3 | V ring of 3.  Then the statistics (keys) or one bit per key tile
-// (queries pass with a mask), and the barriers.
-constexpr int kRingX = 3;
-constexpr int OFF_X_KEYS = 2 * TILE_BYTES, OFF_Y_KEYS = OFF_X_KEYS + kRingX * TILE_BYTES;
-constexpr int OFF_X_QUERIES = TILE_BYTES, OFF_Y_QUERIES = OFF_X_QUERIES + kRingX * TILE_BYTES;
+// Shared memory: seven tiles, keys pass K | V | Q ring of 3 | dO ring of 2, queries pass dO | K ring of 3 |
+// V ring of 2 | output staging; then the row statistics that come with dO (keys pass) and the barriers of
+// either pass.  Q and K are asked for half a tile's time after the sum that frees their stage, so two stages
+// of them leave the tensor core waiting for copies (a ring of 2 for Q: 7.23 against 6.92 ms at 16418 rows).
+constexpr int kRingQ = 3, kRingDO = 2, kRingK = 3, kRingV = 2;
+constexpr int OFF_Q = 2 * TILE_BYTES, OFF_DO = OFF_Q + kRingQ * TILE_BYTES;
+constexpr int OFF_K = TILE_BYTES, OFF_V = OFF_K + kRingK * TILE_BYTES;
+constexpr int OFF_OUT = 6 * TILE_BYTES;
 constexpr int OFF_STAT = 7 * TILE_BYTES;
-constexpr int kTileWords = 256;                    // 8192 tiles = 2^20 keys
-constexpr int OFF_BAR = OFF_STAT + 2 * STAT_BYTES;
-static_assert(kTileWords * 4 <= 2 * STAT_BYTES, "the tile bits take the statistics' place");
-constexpr int SMEM_TOTAL = OFF_BAR + 256;          // the tiles need a base at a multiple of 1024 bytes
+constexpr int OFF_BAR = OFF_STAT + kRingDO * STAT_BYTES;
+constexpr int kBarBytes = 256;
+constexpr int SMEM_TOTAL = OFF_BAR + 2 * kBarBytes;  // the tiles need a base at a multiple of 1024 bytes
+static_assert(OFF_DO + kRingDO * TILE_BYTES == OFF_STAT && OFF_V + kRingV * TILE_BYTES == OFF_OUT, "seven tiles");
+static_assert(SMEM_TOTAL <= 232448, "shared memory of one CTA");
 
 constexpr uint32_t TM_COLS = 512;
 constexpr uint32_t TM_S = 0, TM_DP = 128;
@@ -66,13 +75,50 @@ constexpr uint32_t TM_DQ = 256, TM_Q = 384, TM_DS = 448;   // queries pass
 
 __device__ __forceinline__ float inf() { return __int_as_float(0x7f800000); }
 
-// One half-warp per row of one head: -D_i and minus the base-2 log-sum-exp (negated: the passes add
-// them).  Rows without a valid key and the rows that fill the last tile get -inf, so that
-// exp2(s - lse2) is zero for them.
+// Prepares a call.  One half-warp per row of one head: -D_i and minus the base-2 log-sum-exp (negated: the
+// passes add them).  Rows without a valid key and the rows that fill the last tile get -inf, so that
+// exp2(s - lse2) is zero for them.  With a key mask, the first `batch` blocks list the key tiles of an element
+// that hold a valid key.  The unit counters start at zero.
 __global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const AttnBwdArgs p) {
+  __shared__ int n_listed;
+  __shared__ int ballot_of[8];
   grid_dep_wait();
   grid_dep_launch();
-  const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 4;
+  int block = blockIdx.x;
+  if (block == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0;
+  if (p.key_mask != nullptr) {
+    if (block < p.batch) {
+      const int n_tiles = p.seq_pad / BT;
+      const uint8_t* mask = p.key_mask + (size_t)block * p.seq;
+      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+      if (threadIdx.x == 0) n_listed = 0;
+      for (int t0 = 0; t0 < n_tiles; t0 += 8) {  // eight tiles at a time, one per warp
+        const int t = t0 + warp;
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kc = t * BT + i * 32 + lane;
+          any |= kc < p.seq && mask[kc < p.seq ? kc : 0] != 0;
+        }
+        any = __any_sync(0xffffffffu, any) != 0;
+        if (lane == 0) ballot_of[warp] = any;
+        __syncthreads();
+        if (any && lane == 0) {
+          int at = n_listed;
+          for (int w = 0; w < warp; ++w) at += ballot_of[w];
+          p.tiles[(size_t)block * n_tiles + at] = t;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0)
+          for (int w = 0; w < 8; ++w) n_listed += ballot_of[w];
+        __syncthreads();
+      }
+      if (threadIdx.x == 0) p.n_listed[block] = n_listed;
+      return;
+    }
+    block -= p.batch;
+  }
+  const long long item = ((long long)block * blockDim.x + threadIdx.x) >> 4;
   const int sub = threadIdx.x & 15;
   const long long total = (long long)p.batch * p.seq_pad * p.n_heads;
   if (item >= total) return;
@@ -101,18 +147,60 @@ __global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const AttnBwdArgs p)
 }
 
 struct Bars {
-  uint64_t own_x, own_y;                   // the CTA's own tiles: K / V or (Q in TMEM) / dO
-  uint64_t x_full[kRingX], x_empty[kRingX];  // streamed tiles: Q or K
-  uint64_t y_full[kRingX], y_empty[kRingX];  // dO (2 stages) or V (3)
-  uint64_t first;                          // queries pass: the first K tile has landed and is clean
-  uint64_t s_full, dp_full;                // scores in TMEM
-  uint64_t s_read, dp_read;                // queries pass: scores in registers, and the next K / V landed
-  uint64_t p_full, ds_full;                // P, dS in TMEM; keys pass: and the next Q / dO landed
-  uint64_t acc_done;
+  uint64_t own_x, own_y;           // the CTA's own tiles: K / V or (first unit's Q in TMEM) / dO
+  uint64_t own_x_empty, own_y_empty;
+  uint64_t x_full[3], x_empty[3];  // streamed tiles: Q or K
+  uint64_t y_full[2], y_empty[2];  // dO or V
+  uint64_t first;                  // queries pass: the first K tile has landed and is clean
+  uint64_t s_full, dp_full;        // scores in TMEM
+  uint64_t s_read, dp_read;        // queries pass: scores in registers, and the next K / V landed
+  uint64_t p_full, ds_full;        // P, dS in TMEM; keys pass: and the next Q / dO landed
+  uint64_t acc_done;               // a unit's accumulators are complete
+  uint64_t unit_full[4];
+  int unit[4];                     // the CTA's units in order, -1 behind the last
   uint32_t tmem_slot;
   int abort_flag;
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
+
+// What every role of a pass knows.
+struct Pass {
+  const AttnBwdArgs* p;
+  uint8_t* smem;
+  Bars* bars;
+  volatile int* abort_flag;
+  uint32_t tmem;
+  int n_tiles;   // tiles of a sequence
+  int warp, lane;
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int code) const {
+    return mbar_wait_warp(bar, parity, abort_flag, p->err, DEV_TIMEOUT_ATTN_BWD + code);
+  }
+  // The CTA's k-th unit (-1: none); -2 when the CTA was aborted.  The producer is at most two units ahead
+  // of the slowest role, so four slots need no release.
+  __device__ __forceinline__ int unit(int k) const {
+    if (!wait(&bars->unit_full[k & 3], (uint32_t)((k >> 2) & 1), 1)) return -2;
+    return *reinterpret_cast<volatile int*>(&bars->unit[k & 3]);
+  }
+  __device__ __forceinline__ void publish(int k, int id) const {
+    if (lane == 0) {
+      bars->unit[k & 3] = id;
+      mbar_arrive(&bars->unit_full[k & 3]);
+    }
+    __syncwarp();
+  }
+  // queries pass: key tiles walked for batch element b
+  __device__ __forceinline__ int walked(int b) const { return p->key_mask != nullptr ? p->n_listed[b] : n_tiles; }
+  __device__ __forceinline__ int tile(int b, int n) const {
+    return p->key_mask != nullptr ? p->tiles[(size_t)b * n_tiles + n] : n;
+  }
+};
+
+// Clears the output rows of tile `own` (zeros of a unit without a valid key), by one warp.
+__device__ __forceinline__ void zero_out(__nv_bfloat16* rows, size_t stride, int first, int seq, int lane) {
+  for (int r = first + (lane >> 4); r < first + BT && r < seq; r += 2)
+    *reinterpret_cast<uint4*>(rows + (size_t)r * stride + (lane & 15) * 8) = make_uint4(0, 0, 0, 0);
+}
 
 // Position in a ring of kStages: the stage and the parity of its phase.
 template <int kStages>
@@ -158,185 +246,309 @@ __device__ __forceinline__ void sum_ts(uint32_t d, uint32_t a, uint32_t half_col
                    kIdescSum, (!first || kk > 0) ? 1u : 0u);
 }
 
-// 32 accumulator columns of a row, scaled, as bf16; zeros when the CTA walked no tile.
-__device__ __forceinline__ void store32(__nv_bfloat16* dst, uint32_t src, float f, bool any, bool in_range) {
-  uint32_t x[32];
-  if (any) {
-    tmem_ld32(src, x);
+// 64 accumulator columns of a warp's 32 rows, scaled, as bf16 into its 4 KB of the staging tile
+// (128-byte rows, 16-byte pieces swizzled by the row as the TMA expects).
+__device__ __forceinline__ void stage64(uint8_t* out, uint32_t src, float f, int lane) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t x[32];
+    tmem_ld32(src + c * 32, x);
     tmem_ld_wait();
-  } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = 0u;
+    for (int v = 0; v < 4; ++v) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack_bf16x2(__uint_as_float(x[v * 8 + 2 * e]) * f, __uint_as_float(x[v * 8 + 2 * e + 1]) * f);
+      *reinterpret_cast<uint4*>(out + lane * 128 + (((c * 4 + v) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
-  if (!in_range) return;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = pack_bf16x2(__uint_as_float(x[v * 8 + 2 * e]) * f, __uint_as_float(x[v * 8 + 2 * e + 1]) * f);
-    reinterpret_cast<uint4*>(dst)[v] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 __device__ __forceinline__ f32x2_t pair_of(const uint32_t* x) { return f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])); }
 
 // ------------------------------------------------------------------------------------ keys pass
-// K and V of 128 keys stay; Q and dO of n_tiles query tiles are walked.
-__device__ __forceinline__ void keys_pass(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                          const CUtensorMap& tmDO, const AttnBwdArgs& p, uint8_t* smem, Bars* bars,
-                                          uint32_t tmem, int own, int bh, int n_tiles) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = p.seq;
-  const int b = bh / p.n_heads, h = bh % p.n_heads;
-  volatile int* abort_flag = &bars->abort_flag;
-  int* err = p.err;
-  uint8_t* sK = smem;
-  uint8_t* sV = smem + TILE_BYTES;
-  uint8_t* sQ = smem + OFF_X_KEYS;
-  uint8_t* sDO = smem + OFF_Y_KEYS;
-  float* sStat = reinterpret_cast<float*>(smem + OFF_STAT);
-
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (warp == 0) {
-      if (lane == 0 && n_tiles > 0) {
-        // ---------------------------------------------------------------- TMA producer
-        const float* nl = p.nlse2 + (size_t)bh * p.seq_pad;
-        const float* nd = p.ndelta + (size_t)bh * p.seq_pad;
-        Ring<kRingX> x;
-        Ring<2> y;
-        int nx = 0, ny = 0;
-        mbar_arrive_expect_tx(&bars->own_x, TILE_BYTES);
-        tma_load_3d(sK, &tmK, &bars->own_x, 0, own * BT, bh);
-        tma_load_3d(sK + HALF_BYTES, &tmK, &bars->own_x, 64, own * BT, bh);
-        for (int t = 0; t < n_tiles; ++t) {
-          if (nx >= kRingX && !mbar_wait(&bars->x_empty[x.st], x.ph ^ 1u, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 1)) break;
-          uint8_t* dq = sQ + x.st * TILE_BYTES;
-          mbar_arrive_expect_tx(&bars->x_full[x.st], TILE_BYTES);
-          tma_load_3d(dq, &tmQ, &bars->x_full[x.st], 0, t * BT, bh);
-          tma_load_3d(dq + HALF_BYTES, &tmQ, &bars->x_full[x.st], 64, t * BT, bh);
-          ++nx;
-          x.next();
-          if (t == 0) {
-            mbar_arrive_expect_tx(&bars->own_y, TILE_BYTES);
-            tma_load_4d(sV, &tmV, &bars->own_y, 0, h, own * BT, b);
-            tma_load_4d(sV + HALF_BYTES, &tmV, &bars->own_y, 64, h, own * BT, b);
-          }
-          if (ny >= 2 && !mbar_wait(&bars->y_empty[y.st], y.ph ^ 1u, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 1)) break;
-          uint8_t* dd = sDO + y.st * TILE_BYTES;
-          float* stat = sStat + y.st * (STAT_BYTES / 4);
-          mbar_arrive_expect_tx(&bars->y_full[y.st], TILE_BYTES + STAT_BYTES);
-          bulk_load(stat, nl + t * BT, BT * 4, &bars->y_full[y.st]);
-          bulk_load(stat + BT, nd + t * BT, BT * 4, &bars->y_full[y.st]);
-          tma_load_4d(dd, &tmDO, &bars->y_full[y.st], 0, h, t * BT, b);
-          tma_load_4d(dd + HALF_BYTES, &tmDO, &bars->y_full[y.st], 64, h, t * BT, b);
-          ++ny;
-          y.next();
-        }
-        // drain the copies still in flight (the last use of each barrier phase)
-        mbar_wait_drain(&bars->own_x, 0, err, DEV_TIMEOUT_ATTN_BWD + 2);
-        mbar_wait_drain(&bars->own_y, 0, err, DEV_TIMEOUT_ATTN_BWD + 2);
-        for (int j = nx - kRingX < 0 ? 0 : nx - kRingX; j < nx; ++j)
-          mbar_wait_drain(&bars->x_full[j % kRingX], (uint32_t)((j / kRingX) & 1), err, DEV_TIMEOUT_ATTN_BWD + 2);
-        for (int j = ny - 2 < 0 ? 0 : ny - 2; j < ny; ++j)
-          mbar_wait_drain(&bars->y_full[j & 1], (uint32_t)((j >> 1) & 1), err, DEV_TIMEOUT_ATTN_BWD + 2);
+// A unit: K and V of 128 keys stay; Q and dO of all query tiles are walked.
+__device__ __forceinline__ void keys_producer(const Pass& c, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                              const CUtensorMap& tmV, const CUtensorMap& tmDO) {
+  const AttnBwdArgs& p = *c.p;
+  Bars* bars = c.bars;
+  const int n_units = p.batch * p.n_heads * c.n_tiles;
+  // the next unit that has a valid key
+  auto settle = [&](int id) {
+    while (id < n_units) {
+      if (p.key_mask == nullptr) return id;
+      const int own = id % c.n_tiles, bh = id / c.n_tiles, b = bh / p.n_heads;
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = own * BT + i * 32 + c.lane;
+        any |= key < p.seq && p.key_mask[(size_t)b * p.seq + (key < p.seq ? key : 0)] != 0;
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------------ MMA issuer
-      const uint64_t k_d = sdesc_sw128(smem_u32(sK), 16, 1024), v_d = sdesc_sw128(smem_u32(sV), 16, 1024);
-      const uint64_t q_k = sdesc_sw128(smem_u32(sQ), 16, 1024), do_k = sdesc_sw128(smem_u32(sDO), 16, 1024);
-      const uint64_t q_mn = sdesc_sw128(smem_u32(sQ), HALF_BYTES, 1024), do_mn = sdesc_sw128(smem_u32(sDO), HALF_BYTES, 1024);
-      bool ok = true;
-      if (n_tiles > 0) {
-        ok = mbar_wait_warp(&bars->own_x, 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 3) &&
-             mbar_wait_warp(&bars->x_full[0], 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 3);
-        if (ok) {
-          tc_fence_after();
-          scores_ss(tmem + TM_S, k_d, q_k);
-          tc_commit_warp(&bars->s_full);
-          ok = mbar_wait_warp(&bars->own_y, 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 3) &&
-               mbar_wait_warp(&bars->y_full[0], 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 3);
-        }
-        if (ok) {
-          tc_fence_after();
-          scores_ss(tmem + TM_DP, v_d, do_k);
-          tc_commit_warp(&bars->dp_full);
-        }
-      }
-      int xs = 0;
-      for (int n = 0; ok && n < n_tiles; ++n) {
-        const bool more = n + 1 < n_tiles;
-        const int xn = xs + 1 == kRingX ? 0 : xs + 1;
-        const int ys = n & 1;
-        if (!mbar_wait_warp(&bars->p_full, (uint32_t)(n & 1), abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 4)) break;
-        tc_fence_after();
-        sum_ts(tmem + TM_DV, tmem + TM_S, 64, do_mn + ys * kTile16, n == 0);
-        if (more) {
-          scores_ss(tmem + TM_S, k_d, q_k + xn * kTile16);
-          tc_commit_warp(&bars->s_full);
-        }
-        if (!mbar_wait_warp(&bars->ds_full, (uint32_t)(n & 1), abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 5)) break;
-        tc_fence_after();
-        sum_ts(tmem + TM_DK, tmem + TM_DP, 64, q_mn + xs * kTile16, n == 0);
-        tc_commit_warp(&bars->x_empty[xs]);
-        tc_commit_warp(&bars->y_empty[ys]);
-        if (more) {
-          scores_ss(tmem + TM_DP, v_d, do_k + (ys ^ 1) * kTile16);
-          tc_commit_warp(&bars->dp_full);
-        }
-        xs = xn;
-      }
-      tc_commit_warp(&bars->acc_done);
-      mbar_wait_drain(&bars->acc_done, 0, err, DEV_TIMEOUT_ATTN_BWD + 6);
-    } else if (warp == 2) {
-      // ------------------------------------------------------------------ wait proxy
-      Ring<kRingX> x;
-      Ring<2> y;
-      for (int n = 0; n < n_tiles; ++n) {
-        const bool more = n + 1 < n_tiles;
-        x.next();
-        y.next();
-        // each arrival belongs to the barrier's phase n: phase n - 1 must be complete first
-        const uint32_t prev = (uint32_t)((n - 1) & 1);
-        if ((n > 0 && !mbar_wait_warp(&bars->p_full, prev, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 7)) ||
-            (more && !mbar_wait_warp(&bars->x_full[x.st], x.ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 7)))
-          break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full);
-        if ((n > 0 && !mbar_wait_warp(&bars->ds_full, prev, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 8)) ||
-            (more && !mbar_wait_warp(&bars->y_full[y.st], y.ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 8)))
-          break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->ds_full);
-      }
+      if (__any_sync(0xffffffffu, any)) return id;
+      zero_out(p.dkp + (size_t)bh * p.seq * kHeadDim, kHeadDim, own * BT, p.seq, c.lane);
+      zero_out(p.dv + (size_t)b * p.seq * 3 * p.n_heads * kHeadDim + (size_t)(bh % p.n_heads) * kHeadDim,
+               (size_t)3 * p.n_heads * kHeadDim, own * BT, p.seq, c.lane);
+      if (c.lane == 0) id = (int)gridDim.x + atomicAdd(p.counters, 1);
+      id = __shfl_sync(0xffffffffu, id, 0);
     }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
-    // ------------------------------------------------------------------ P and dS
-    const int half = (warp - 4) >> 2;            // query half of this warpgroup
-    const int r = (warp & 3) * 32 + lane;        // TMEM lane: key of the tile
-    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = t_row + TM_S + (uint32_t)half * 64u, t_dp = t_row + TM_DP + (uint32_t)half * 64u;
-    const int row = own * BT + r;
-    const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + (size_t)b * S : nullptr;
-    const bool row_ok = row < S && (mask == nullptr || mask[row] != 0);
-    const bool rows_ok = __all_sync(0xffffffffu, row_ok) != 0;
-    const f32x2_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2);
-    bool ok = true;
-    for (int n = 0; n < n_tiles; ++n) {
-      const int st = n & 1;
-      const uint32_t ph = (uint32_t)(n & 1);
-      // the statistics land with dO, well before the scores are there
-      if (!mbar_wait_warp(&bars->y_full[st], (uint32_t)((n >> 1) & 1), abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 9)) {
+    return -1;
+  };
+  auto take = [&] {
+    int id = 0;
+    if (c.lane == 0) id = (int)gridDim.x + atomicAdd(p.counters, 1);
+    return settle(__shfl_sync(0xffffffffu, id, 0));
+  };
+  Ring<kRingQ> x;
+  Ring<kRingDO> y;
+  int nx = 0, ny = 0, nown_x = 0, nown_y = 0;
+  bool ok = true;
+  int id = settle((int)blockIdx.x);
+  c.publish(0, id);
+  for (int k = 0; ok && id >= 0; ++k) {
+    const int own = id % c.n_tiles, bh = id / c.n_tiles;
+    const int b = bh / p.n_heads, h = bh % p.n_heads;
+    const float* nl = p.nlse2 + (size_t)bh * p.seq_pad;
+    const float* nd = p.ndelta + (size_t)bh * p.seq_pad;
+    int next_id = -1;
+    if (k > 0 && !c.wait(&bars->own_x_empty, (uint32_t)((k - 1) & 1), 2)) break;
+    if (c.lane == 0) {
+      mbar_arrive_expect_tx(&bars->own_x, TILE_BYTES);
+      tma_load_3d(c.smem, &tmK, &bars->own_x, 0, own * BT, bh);
+      tma_load_3d(c.smem + HALF_BYTES, &tmK, &bars->own_x, 64, own * BT, bh);
+    }
+    ++nown_x;
+    for (int t = 0; t < c.n_tiles; ++t) {
+      if (nx >= kRingQ && !c.wait(&bars->x_empty[x.st], x.ph ^ 1u, 2)) {
         ok = false;
         break;
       }
-      const float4* stat = reinterpret_cast<const float4*>(sStat + st * (STAT_BYTES / 4) + half * 64);
+      if (c.lane == 0) {
+        uint8_t* dq = c.smem + OFF_Q + x.st * TILE_BYTES;
+        mbar_arrive_expect_tx(&bars->x_full[x.st], TILE_BYTES);
+        tma_load_3d(dq, &tmQ, &bars->x_full[x.st], 0, t * BT, bh);
+        tma_load_3d(dq + HALF_BYTES, &tmQ, &bars->x_full[x.st], 64, t * BT, bh);
+      }
+      ++nx;
+      x.next();
+      if (t == 0) {
+        if (k > 0 && !c.wait(&bars->own_y_empty, (uint32_t)((k - 1) & 1), 2)) {
+          ok = false;
+          break;
+        }
+        if (c.lane == 0) {
+          mbar_arrive_expect_tx(&bars->own_y, TILE_BYTES);
+          tma_load_4d(c.smem + TILE_BYTES, &tmV, &bars->own_y, 0, h, own * BT, b);
+          tma_load_4d(c.smem + TILE_BYTES + HALF_BYTES, &tmV, &bars->own_y, 64, h, own * BT, b);
+        }
+        ++nown_y;
+      }
+      if (ny >= kRingDO && !c.wait(&bars->y_empty[y.st], y.ph ^ 1u, 2)) {
+        ok = false;
+        break;
+      }
+      if (c.lane == 0) {
+        uint8_t* dd = c.smem + OFF_DO + y.st * TILE_BYTES;
+        float* stat = reinterpret_cast<float*>(c.smem + OFF_STAT + y.st * STAT_BYTES);
+        mbar_arrive_expect_tx(&bars->y_full[y.st], TILE_BYTES + STAT_BYTES);
+        bulk_load(stat, nl + t * BT, BT * 4, &bars->y_full[y.st]);
+        bulk_load(stat + BT, nd + t * BT, BT * 4, &bars->y_full[y.st]);
+        tma_load_4d(dd, &tmDO, &bars->y_full[y.st], 0, h, t * BT, b);
+        tma_load_4d(dd + HALF_BYTES, &tmDO, &bars->y_full[y.st], 64, h, t * BT, b);
+      }
+      ++ny;
+      y.next();
+      if (t == (c.n_tiles > 1 ? 1 : 0)) {  // the next unit, before anyone asks for it
+        next_id = take();
+        c.publish(k + 1, next_id);
+      }
+    }
+    id = next_id;
+  }
+  // drain the copies still in flight (the last use of each barrier phase)
+  if (nown_x > 0) mbar_wait_drain(&bars->own_x, (uint32_t)((nown_x - 1) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+  if (nown_y > 0) mbar_wait_drain(&bars->own_y, (uint32_t)((nown_y - 1) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+  for (int j = nx - kRingQ < 0 ? 0 : nx - kRingQ; j < nx; ++j)
+    mbar_wait_drain(&bars->x_full[j % kRingQ], (uint32_t)((j / kRingQ) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+  for (int j = ny - kRingDO < 0 ? 0 : ny - kRingDO; j < ny; ++j)
+    mbar_wait_drain(&bars->y_full[j % kRingDO], (uint32_t)((j / kRingDO) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+}
+
+__device__ __forceinline__ void keys_mma(const Pass& c) {
+  Bars* bars = c.bars;
+  const uint32_t tmem = c.tmem;
+  const uint32_t sm = smem_u32(c.smem);
+  const uint64_t k_d = sdesc_sw128(sm, 16, 1024), v_d = sdesc_sw128(sm + TILE_BYTES, 16, 1024);
+  const uint64_t q_k = sdesc_sw128(sm + OFF_Q, 16, 1024), do_k = sdesc_sw128(sm + OFF_DO, 16, 1024);
+  const uint64_t q_mn = sdesc_sw128(sm + OFF_Q, HALF_BYTES, 1024), do_mn = sdesc_sw128(sm + OFF_DO, HALF_BYTES, 1024);
+  const int last = c.n_tiles - 1;
+  int id = c.unit(0);
+  bool ok = id >= 0;
+  if (ok) {
+    ok = c.wait(&bars->own_x, 0, 4) && c.wait(&bars->x_full[0], 0, 4);
+    if (ok) {
+      tc_fence_after();
+      scores_ss(tmem + TM_S, k_d, q_k);
+      tc_commit_warp(&bars->s_full);
+      if (last == 0) tc_commit_warp(&bars->own_x_empty);
+      ok = c.wait(&bars->own_y, 0, 4) && c.wait(&bars->y_full[0], 0, 4);
+    }
+    if (ok) {
+      tc_fence_after();
+      scores_ss(tmem + TM_DP, v_d, do_k);
+      tc_commit_warp(&bars->dp_full);
+      if (last == 0) tc_commit_warp(&bars->own_y_empty);
+    }
+  }
+  uint32_t g = 0;  // tiles so far, over all units: phases, and the dO stage
+  uint32_t qs = 0;  // Q stage
+  for (int k = 0; ok && id >= 0; ++k) {
+    for (int n = 0; n <= last; ++n, ++g) {
+      if (n == last) {
+        id = c.unit(k + 1);
+        if (id == -2) {
+          ok = false;
+          break;
+        }
+      }
+      const bool more = id >= 0;                                  // a tile follows
+      const bool next_last = n == last ? last == 0 : n + 1 == last;  // and is the last of its unit
+      const uint32_t st = g & 1u, ph = g & 1u;
+      const uint32_t qn = qs + 1 == kRingQ ? 0 : qs + 1;
+      // P of this tile, and Q of the next (and its K, for a new unit) landed; P of a unit's first tile is
+      // released when the accumulators of the unit before have been read
+      if (!c.wait(&bars->p_full, ph, 5)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      sum_ts(tmem + TM_DV, tmem + TM_S, 64, do_mn + st * kTile16, n == 0);
+      if (more) {
+        scores_ss(tmem + TM_S, k_d, q_k + qn * kTile16);
+        tc_commit_warp(&bars->s_full);
+        if (next_last) tc_commit_warp(&bars->own_x_empty);
+      }
+      if (!c.wait(&bars->ds_full, ph, 6)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      sum_ts(tmem + TM_DK, tmem + TM_DP, 64, q_mn + qs * kTile16, n == 0);
+      tc_commit_warp(&bars->x_empty[qs]);
+      tc_commit_warp(&bars->y_empty[st]);
+      if (n == last) tc_commit_warp(&bars->acc_done);
+      if (more) {
+        scores_ss(tmem + TM_DP, v_d, do_k + (st ^ 1u) * kTile16);
+        tc_commit_warp(&bars->dp_full);
+        if (next_last) tc_commit_warp(&bars->own_y_empty);
+      }
+      qs = qn;
+    }
+  }
+}
+
+__device__ __forceinline__ void keys_proxy(const Pass& c) {
+  Bars* bars = c.bars;
+  int id = c.unit(0);
+  bool ok = true;
+  uint32_t g = 0;
+  Ring<kRingQ> x;
+  for (int k = 0; ok && id >= 0; ++k) {
+    for (int n = 0; n < c.n_tiles; ++n, ++g) {
+      x.next();
+      const bool turn = n + 1 == c.n_tiles;  // the next tile is a new unit's
+      if (turn) {
+        id = c.unit(k + 1);
+        if (id == -2) {
+          ok = false;
+          break;
+        }
+      }
+      const bool more = id >= 0;
+      const uint32_t st = (g + 1) & 1u, ph = ((g + 1) >> 1) & 1u;
+      // each arrival belongs to the barrier's phase g: phase g - 1 must be complete first
+      const uint32_t prev = (g - 1) & 1u;
+      if ((g > 0 && !c.wait(&bars->p_full, prev, 7)) || (more && turn && !c.wait(&bars->own_x, (uint32_t)((k + 1) & 1), 7)) ||
+          (more && !c.wait(&bars->x_full[x.st], x.ph, 7))) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive(&bars->p_full);
+      if ((g > 0 && !c.wait(&bars->ds_full, prev, 8)) || (more && turn && !c.wait(&bars->own_y, (uint32_t)((k + 1) & 1), 8)) ||
+          (more && !c.wait(&bars->y_full[st], ph, 8))) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive(&bars->ds_full);
+    }
+  }
+}
+
+// Warpgroup 0 stores dV, warpgroup 1 dK: first the row's accumulators as bf16 into registers (after which
+// they may be overwritten), then to memory.
+__device__ __forceinline__ void keys_read(uint32_t src, float f, uint32_t (&w)[64]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t x[32];
+    tmem_ld32(src + j * 32, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      w[16 * j + i] = pack_bf16x2(__uint_as_float(x[2 * i]) * f, __uint_as_float(x[2 * i + 1]) * f);
+  }
+}
+
+__device__ __forceinline__ void keys_store(const Pass& c, int id, int half, const uint32_t (&w)[64]) {
+  const AttnBwdArgs& p = *c.p;
+  const int row = (id % c.n_tiles) * BT + (c.warp & 3) * 32 + c.lane, bh = id / c.n_tiles;
+  if (row >= p.seq) return;
+  __nv_bfloat16* dst = half == 0 ? p.dv + ((size_t)(bh / p.n_heads) * p.seq + row) * 3 * p.n_heads * kHeadDim +
+                                       (size_t)(bh % p.n_heads) * kHeadDim
+                                 : p.dkp + ((size_t)bh * p.seq + row) * kHeadDim;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+__device__ __forceinline__ void keys_compute(const Pass& c) {
+  const AttnBwdArgs& p = *c.p;
+  Bars* bars = c.bars;
+  const int half = (c.warp - 4) >> 2;          // query half of this warpgroup
+  const int r = (c.warp & 3) * 32 + c.lane;    // TMEM lane: key of the tile
+  const uint32_t t_row = c.tmem + ((uint32_t)((c.warp & 3) * 32) << 16);
+  const uint32_t t_s = t_row + TM_S + (uint32_t)half * 64u, t_dp = t_row + TM_DP + (uint32_t)half * 64u;
+  const uint32_t t_acc = t_row + (half == 0 ? TM_DV : TM_DK);
+  const float f_acc = half == 0 ? 1.0f : p.scale;
+  const f32x2_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2);
+  int before = -1;                             // the unit whose accumulators are still to be read
+  bool ok = true;
+  uint32_t g = 0;
+  for (int k = 0; ok; ++k) {
+    const int id = c.unit(k);
+    if (id < 0) {
+      ok = id != -2;
+      break;
+    }
+    const int row = (id % c.n_tiles) * BT + r;
+    bool row_ok = row < p.seq;
+    if (row_ok && p.key_mask != nullptr) row_ok = p.key_mask[(size_t)(id / c.n_tiles / p.n_heads) * p.seq + row] != 0;
+    const bool rows_ok = __all_sync(0xffffffffu, row_ok) != 0;
+    for (int n = 0; n < c.n_tiles; ++n, ++g) {
+      const uint32_t st = g & 1u, ph = g & 1u;
+      // the statistics land with dO, well before the scores are there
+      if (!c.wait(&bars->y_full[st], (g >> 1) & 1u, 9)) {
+        ok = false;
+        break;
+      }
+      const float4* stat = reinterpret_cast<const float4*>(c.smem + OFF_STAT + st * STAT_BYTES) + half * 16;
       float4 nl[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) nl[i] = stat[i];
-      if (!mbar_wait_warp(&bars->s_full, ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 10)) {
+      if (!c.wait(&bars->s_full, ph, 10)) {
         ok = false;
         break;
       }
@@ -361,252 +573,374 @@ __device__ __forceinline__ void keys_pass(const CUtensorMap& tmQ, const CUtensor
       for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(__uint_as_float(pr[2 * i]), __uint_as_float(pr[2 * i + 1]));
       tmem_st32(t_s, pk);
       tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->p_full);
+      if (n == 0 && before >= 0) {
+        if (!c.wait(&bars->acc_done, (uint32_t)((k - 1) & 1), 11)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t w[64];
+        keys_read(t_acc, f_acc, w);
+        tc_fence_before();
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive(&bars->p_full);
+        keys_store(c, before, half, w);
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive(&bars->p_full);
+      }
       float4 nd[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) nd[i] = stat[32 + i];
-      if (!mbar_wait_warp(&bars->dp_full, ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 11)) {
+      if (!c.wait(&bars->dp_full, ph, 12)) {
         ok = false;
         break;
       }
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int j = 0; j < 2; ++j) {
         uint32_t dp[32];
-        tmem_ld32(t_dp + 32 * c, dp);
-        if (c == 1) {
+        tmem_ld32(t_dp + 32 * j, dp);
+        if (j == 1) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) nd[i] = stat[40 + i];
         }
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 d = nd[i];
           float z[4];
-          f2_unpack(f2_mul(f2_add(pair_of(dp + 4 * i), f2_pack(d.x, d.y)), pair_of(pr + 32 * c + 4 * i)), z[0], z[1]);
-          f2_unpack(f2_mul(f2_add(pair_of(dp + 4 * i + 2), f2_pack(d.z, d.w)), pair_of(pr + 32 * c + 4 * i + 2)), z[2], z[3]);
+          f2_unpack(f2_mul(f2_add(pair_of(dp + 4 * i), f2_pack(nd[i].x, nd[i].y)), pair_of(pr + 32 * j + 4 * i)), z[0], z[1]);
+          f2_unpack(f2_mul(f2_add(pair_of(dp + 4 * i + 2), f2_pack(nd[i].z, nd[i].w)), pair_of(pr + 32 * j + 4 * i + 2)), z[2],
+                    z[3]);
           if (!rows_ok) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[e] = row_ok ? z[e] : 0.0f;
           }
-          pk[16 * c + 2 * i] = pack_bf16x2(z[0], z[1]);
-          pk[16 * c + 2 * i + 1] = pack_bf16x2(z[2], z[3]);
+          pk[16 * j + 2 * i] = pack_bf16x2(z[0], z[1]);
+          pk[16 * j + 2 * i + 1] = pack_bf16x2(z[2], z[3]);
         }
       }
       tmem_st32(t_dp, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->ds_full);
+      if (c.lane == 0) mbar_arrive(&bars->ds_full);
     }
-    // warpgroup 0 stores dV, warpgroup 1 dK
-    if (ok && n_tiles > 0) ok = mbar_wait_warp(&bars->acc_done, 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 12);
-    if (ok) {
-      tc_fence_after();
-      __nv_bfloat16* dst = half == 0 ? p.dv + ((size_t)b * S + row) * 3 * p.n_heads * kHeadDim + (size_t)h * kHeadDim
-                                     : p.dkp + ((size_t)bh * S + row) * kHeadDim;
-      const uint32_t src = t_row + (half == 0 ? TM_DV : TM_DK);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) store32(dst + c * 32, src + c * 32, half == 0 ? 1.0f : p.scale, n_tiles > 0, row < S);
-      tc_fence_before();
+    before = id;
+    if (!ok) break;
+    // the last unit's accumulators (any other's are read behind the next unit's first scores)
+    const int next_id = c.unit(k + 1);
+    if (next_id < 0) {
+      if (next_id == -1 && c.wait(&bars->acc_done, (uint32_t)(k & 1), 13)) {
+        tc_fence_after();
+        uint32_t w[64];
+        keys_read(t_acc, f_acc, w);
+        keys_store(c, id, half, w);
+      }
+      break;
     }
   }
+  tc_fence_before();
 }
 
 // ------------------------------------------------------------------------------------ queries pass
-// Q (in TMEM) and dO of 128 queries stay; K and V of the key tiles are walked, those without a valid key
-// left out.
-__device__ __forceinline__ void queries_pass(const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmDO,
-                                             const AttnBwdArgs& p, uint8_t* smem, Bars* bars, uint32_t tmem, int own,
-                                             int bh, int n_tiles) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = p.seq;
-  const int b = bh / p.n_heads, h = bh % p.n_heads;
-  const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + (size_t)b * S : nullptr;
-  volatile int* abort_flag = &bars->abort_flag;
-  int* err = p.err;
-  uint8_t* sDO = smem;
-  uint8_t* sK = smem + OFF_X_QUERIES;
-  uint8_t* sV = smem + OFF_Y_QUERIES;
-  const uint32_t* tile_any = reinterpret_cast<const uint32_t*>(smem + OFF_STAT);
-  auto next = [&](int t) {  // first tile from t on that is walked
-    if (mask != nullptr)
-      while (t < n_tiles && !((tile_any[t >> 5] >> (t & 31)) & 1u)) ++t;
-    return t;
+// A unit: Q (in TMEM) and dO of 128 queries stay; K and V of the key tiles with a valid key are walked.
+__device__ __forceinline__ void queries_producer(const Pass& c, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                                 const CUtensorMap& tmDO) {
+  const AttnBwdArgs& p = *c.p;
+  Bars* bars = c.bars;
+  const int n_units = p.batch * p.n_heads * c.n_tiles;
+  const int fixed = (int)gridDim.x > n_units ? (int)gridDim.x - n_units : 0;  // CTAs that start with a unit of this pass
+  auto draw = [&] {
+    int id = 0;
+    if (c.lane == 0) id = fixed + atomicAdd(p.counters + 1, 1);
+    return __shfl_sync(0xffffffffu, id, 0);
   };
-
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (warp == 0) {
-      if (lane == 0 && next(0) < n_tiles) {
-        // ---------------------------------------------------------------- TMA producer
-        Ring<kRingX> x;
-        int nx = 0, ny = 0;
-        bool own_sent = false;
-        for (int t = next(0); t < n_tiles; t = next(t + 1), x.next()) {
-          if (nx >= kRingX && !mbar_wait(&bars->x_empty[x.st], x.ph ^ 1u, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 1)) break;
-          uint8_t* dk = sK + x.st * TILE_BYTES;
-          mbar_arrive_expect_tx(&bars->x_full[x.st], TILE_BYTES);
-          tma_load_3d(dk, &tmK, &bars->x_full[x.st], 0, t * BT, bh);
-          tma_load_3d(dk + HALF_BYTES, &tmK, &bars->x_full[x.st], 64, t * BT, bh);
-          ++nx;
-          if (!own_sent) {
-            own_sent = true;
-            mbar_arrive_expect_tx(&bars->own_y, TILE_BYTES);
-            tma_load_4d(sDO, &tmDO, &bars->own_y, 0, h, own * BT, b);
-            tma_load_4d(sDO + HALF_BYTES, &tmDO, &bars->own_y, 64, h, own * BT, b);
-          }
-          if (ny >= kRingX && !mbar_wait(&bars->y_empty[x.st], x.ph ^ 1u, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 1)) break;
-          uint8_t* dv = sV + x.st * TILE_BYTES;
-          mbar_arrive_expect_tx(&bars->y_full[x.st], TILE_BYTES);
-          tma_load_4d(dv, &tmV, &bars->y_full[x.st], 0, h, t * BT, b);
-          tma_load_4d(dv + HALF_BYTES, &tmV, &bars->y_full[x.st], 64, h, t * BT, b);
-          ++ny;
-        }
-        mbar_wait_drain(&bars->own_y, 0, err, DEV_TIMEOUT_ATTN_BWD + 2);
-        for (int j = nx - kRingX < 0 ? 0 : nx - kRingX; j < nx; ++j)
-          mbar_wait_drain(&bars->x_full[j % kRingX], (uint32_t)((j / kRingX) & 1), err, DEV_TIMEOUT_ATTN_BWD + 2);
-        for (int j = ny - kRingX < 0 ? 0 : ny - kRingX; j < ny; ++j)
-          mbar_wait_drain(&bars->y_full[j % kRingX], (uint32_t)((j / kRingX) & 1), err, DEV_TIMEOUT_ATTN_BWD + 2);
+  auto settle = [&](int id) {
+    while (id < n_units) {
+      const int own = id % c.n_tiles, bh = id / c.n_tiles;
+      if (c.walked(bh / p.n_heads) > 0) return id;
+      zero_out(p.dqp + (size_t)bh * p.seq * kHeadDim, kHeadDim, own * BT, p.seq, c.lane);
+      id = draw();
+    }
+    return -1;
+  };
+  Ring<kRingK> x;
+  Ring<kRingV> y;
+  int nx = 0, ny = 0, nown = 0;
+  bool ok = true;
+  int id = settle((int)blockIdx.x >= n_units ? (int)blockIdx.x - n_units : draw());
+  c.publish(0, id);
+  for (int k = 0; ok && id >= 0; ++k) {
+    const int own = id % c.n_tiles, bh = id / c.n_tiles;
+    const int b = bh / p.n_heads, h = bh % p.n_heads;
+    const int count = c.walked(b);
+    int next_id = -1;
+    int t1 = c.tile(b, 0);
+    for (int n = 0; n < count; ++n) {
+      const int t = t1;
+      if (n + 1 < count) t1 = c.tile(b, n + 1);
+      if (nx >= kRingK && !c.wait(&bars->x_empty[x.st], x.ph ^ 1u, 2)) {
+        ok = false;
+        break;
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------------ MMA issuer
-      const uint64_t do_d = sdesc_sw128(smem_u32(sDO), 16, 1024);
-      const uint64_t k_k = sdesc_sw128(smem_u32(sK), 16, 1024), v_k = sdesc_sw128(smem_u32(sV), 16, 1024);
-      const uint64_t k_mn = sdesc_sw128(smem_u32(sK), HALF_BYTES, 1024);
-      int t = next(0);
-      bool ok = true;
-      if (t < n_tiles) {
-        ok = mbar_wait_warp(&bars->own_x, 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 3) &&
-             mbar_wait_warp(&bars->first, 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 3);
-        if (ok) {
-          tc_fence_after();
-          scores_ts(tmem + TM_S, tmem + TM_Q, k_k);
-          tc_commit_warp(&bars->s_full);
-          ok = mbar_wait_warp(&bars->own_y, 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 3) &&
-               mbar_wait_warp(&bars->y_full[0], 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 3);
-        }
-        if (ok) {
-          tc_fence_after();
-          scores_ss(tmem + TM_DP, do_d, v_k);
-          tc_commit_warp(&bars->dp_full);
-          tc_commit_warp(&bars->y_empty[0]);
-        }
+      if (c.lane == 0) {
+        uint8_t* dk = c.smem + OFF_K + x.st * TILE_BYTES;
+        mbar_arrive_expect_tx(&bars->x_full[x.st], TILE_BYTES);
+        tma_load_3d(dk, &tmK, &bars->x_full[x.st], 0, t * BT, bh);
+        tma_load_3d(dk + HALF_BYTES, &tmK, &bars->x_full[x.st], 64, t * BT, bh);
       }
-      int st = 0;
-      for (int n = 0; ok && t < n_tiles; ++n) {
-        const int t1 = next(t + 1);
-        const bool more = t1 < n_tiles;
-        const int sn = st + 1 == kRingX ? 0 : st + 1;
-        const uint32_t ph = (uint32_t)(n & 1);
-        if (more) {
-          if (!mbar_wait_warp(&bars->s_read, ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 4)) break;
-          tc_fence_after();
-          scores_ts(tmem + TM_S, tmem + TM_Q, k_k + sn * kTile16);
-          tc_commit_warp(&bars->s_full);
-          if (!mbar_wait_warp(&bars->dp_read, ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 4)) break;
-          tc_fence_after();
-          scores_ss(tmem + TM_DP, do_d, v_k + sn * kTile16);
-          tc_commit_warp(&bars->dp_full);
-          tc_commit_warp(&bars->y_empty[sn]);
-        }
-        if (!mbar_wait_warp(&bars->ds_full, ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 5)) break;
-        tc_fence_after();
-        sum_ts(tmem + TM_DQ, tmem + TM_DS, 32, k_mn + st * kTile16, n == 0);
-        tc_commit_warp(&bars->x_empty[st]);
-        st = sn;
-        t = t1;
-      }
-      tc_commit_warp(&bars->acc_done);
-      mbar_wait_drain(&bars->acc_done, 0, err, DEV_TIMEOUT_ATTN_BWD + 6);
-    } else if (warp == 2) {
-      // ------------------------------------------------------------------ wait proxy, cleaner
-      Ring<kRingX> x;
-      int n = 0;
-      for (int t = next(0); t < n_tiles; ++n, x.next()) {
-        // K of this tile, clean, for S_n: an arrival of phase n - 1 of s_read (phase n - 2 complete)
-        uint32_t bad[4] = {0, 0, 0, 0};
-        if (mask != nullptr) masked_keys(mask, t * BT, S, lane, bad);
-        if ((n > 1 && !mbar_wait_warp(&bars->s_read, (uint32_t)(n & 1), abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 7)) ||
-            !mbar_wait_warp(&bars->x_full[x.st], x.ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 7))
+      ++nx;
+      x.next();
+      if (n == 0) {
+        if (k > 0 && !c.wait(&bars->own_y_empty, (uint32_t)((k - 1) & 1), 2)) {
+          ok = false;
           break;
-        zero_rows(sK + x.st * TILE_BYTES, bad, lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(n == 0 ? &bars->first : &bars->s_read);
-        // V of this tile, for dP_n
-        if (n > 0) {
-          if ((n > 1 && !mbar_wait_warp(&bars->dp_read, (uint32_t)(n & 1), abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 8)) ||
-              !mbar_wait_warp(&bars->y_full[x.st], x.ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 8))
-            break;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->dp_read);
         }
-        t = next(t + 1);
+        if (c.lane == 0) {
+          mbar_arrive_expect_tx(&bars->own_y, TILE_BYTES);
+          tma_load_4d(c.smem, &tmDO, &bars->own_y, 0, h, own * BT, b);
+          tma_load_4d(c.smem + HALF_BYTES, &tmDO, &bars->own_y, 64, h, own * BT, b);
+        }
+        ++nown;
+      }
+      if (ny >= kRingV && !c.wait(&bars->y_empty[y.st], y.ph ^ 1u, 2)) {
+        ok = false;
+        break;
+      }
+      if (c.lane == 0) {
+        uint8_t* dv = c.smem + OFF_V + y.st * TILE_BYTES;
+        mbar_arrive_expect_tx(&bars->y_full[y.st], TILE_BYTES);
+        tma_load_4d(dv, &tmV, &bars->y_full[y.st], 0, h, t * BT, b);
+        tma_load_4d(dv + HALF_BYTES, &tmV, &bars->y_full[y.st], 64, h, t * BT, b);
+      }
+      ++ny;
+      y.next();
+      if (n == (count > 1 ? 1 : 0)) {
+        next_id = settle(draw());
+        c.publish(k + 1, next_id);
       }
     }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
-    // ------------------------------------------------------------------ dS
-    const int half = (warp - 4) >> 2;            // key half of this warpgroup
-    const int r = (warp & 3) * 32 + lane;        // TMEM lane: query of the tile
-    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = t_row + TM_S + (uint32_t)half * 64u, t_dp = t_row + TM_DP + (uint32_t)half * 64u;
-    const uint32_t t_ds = t_row + TM_DS + (uint32_t)half * 32u;
-    const int row = own * BT + r;
-    const f32x2_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2);
-    {
-      // this row's half of Q to TMEM: element d in column d / 2, as in memory
-      uint32_t q[32];
-      const uint4* src = reinterpret_cast<const uint4*>(p.qp + ((size_t)bh * S + (row < S ? row : 0)) * kHeadDim + half * 64);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 v = row < S ? src[i] : make_uint4(0, 0, 0, 0);
-        q[4 * i] = v.x;
-        q[4 * i + 1] = v.y;
-        q[4 * i + 2] = v.z;
-        q[4 * i + 3] = v.w;
-      }
-      tmem_st32(t_row + TM_Q + (uint32_t)half * 32u, q);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->own_x);
+    id = next_id;
+  }
+  if (nown > 0) mbar_wait_drain(&bars->own_y, (uint32_t)((nown - 1) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+  for (int j = nx - kRingK < 0 ? 0 : nx - kRingK; j < nx; ++j)
+    mbar_wait_drain(&bars->x_full[j % kRingK], (uint32_t)((j / kRingK) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+  for (int j = ny - kRingV < 0 ? 0 : ny - kRingV; j < ny; ++j)
+    mbar_wait_drain(&bars->y_full[j % kRingV], (uint32_t)((j / kRingV) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+}
+
+__device__ __forceinline__ void queries_mma(const Pass& c) {
+  Bars* bars = c.bars;
+  const uint32_t tmem = c.tmem;
+  const uint32_t sm = smem_u32(c.smem);
+  const uint64_t do_d = sdesc_sw128(sm, 16, 1024);
+  const uint64_t k_k = sdesc_sw128(sm + OFF_K, 16, 1024), v_k = sdesc_sw128(sm + OFF_V, 16, 1024);
+  const uint64_t k_mn = sdesc_sw128(sm + OFF_K, HALF_BYTES, 1024);
+  int id = c.unit(0);
+  bool ok = id >= 0;
+  int count = ok ? c.walked(id / c.n_tiles / c.p->n_heads) : 0;
+  if (ok) {
+    ok = c.wait(&bars->own_x, 0, 4) && c.wait(&bars->first, 0, 4);
+    if (ok) {
+      tc_fence_after();
+      scores_ts(tmem + TM_S, tmem + TM_Q, k_k);
+      tc_commit_warp(&bars->s_full);
+      ok = c.wait(&bars->own_y, 0, 4) && c.wait(&bars->y_full[0], 0, 4);
     }
-    const float nl = p.nlse2[(size_t)bh * p.seq_pad + row], nd = p.ndelta[(size_t)bh * p.seq_pad + row];
-    const f32x2_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
-    // may this lane's two keys of the tile be attended to (read a tile ahead)
-    bool key[2] = {true, true};
-    auto read_mask = [&](int t) {
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int kc = t * BT + half * 64 + w * 32 + lane;
-        key[w] = kc < S && (mask == nullptr || mask[kc < S ? kc : 0] != 0);
+    if (ok) {
+      tc_fence_after();
+      scores_ss(tmem + TM_DP, do_d, v_k);
+      tc_commit_warp(&bars->dp_full);
+      tc_commit_warp(&bars->y_empty[0]);
+      if (count == 1) tc_commit_warp(&bars->own_y_empty);
+    }
+  }
+  uint32_t g = 0;
+  int st = 0;
+  for (int k = 0; ok && id >= 0; ++k) {
+    const int here = count;
+    for (int n = 0; n < here; ++n, ++g) {
+      if (n + 1 == here) {
+        id = c.unit(k + 1);
+        if (id == -2) {
+          ok = false;
+          break;
+        }
+        if (id >= 0) count = c.walked(id / c.n_tiles / c.p->n_heads);
       }
-    };
-    bool ok = true;
-    int n = 0;
-    Ring<kRingX> before;  // stage and phase of the tile before this one
-    int t = next(0);
-    if (t < n_tiles) read_mask(t);
-    for (int t1; t < n_tiles; t = t1, ++n) {
-      const uint32_t ph = (uint32_t)(n & 1);
-      t1 = next(t + 1);
-      const uint32_t valid[2] = {__ballot_sync(0xffffffffu, key[0]), __ballot_sync(0xffffffffu, key[1])};
-      if (t1 < n_tiles) read_mask(t1);
-      if (!mbar_wait_warp(&bars->s_full, ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 10)) {
+      const bool next_last = n + 1 == here ? count == 1 : n + 2 == here;
+      const int sn = st + 1 == kRingK ? 0 : st + 1;
+      const uint32_t ph = g & 1u, vn = (g + 1) & 1u;
+      if (id >= 0) {
+        // the scores are in registers and K of the next tile has landed, clean (and its Q is in TMEM)
+        if (!c.wait(&bars->s_read, ph, 5)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        scores_ts(tmem + TM_S, tmem + TM_Q, k_k + (uint32_t)sn * kTile16);
+        tc_commit_warp(&bars->s_full);
+        if (!c.wait(&bars->dp_read, ph, 5)) {  // and V (and dO)
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        scores_ss(tmem + TM_DP, do_d, v_k + vn * kTile16);
+        tc_commit_warp(&bars->dp_full);
+        tc_commit_warp(&bars->y_empty[vn]);
+        if (next_last) tc_commit_warp(&bars->own_y_empty);
+      }
+      // dS of a unit's first tile is released when dQ of the unit before has been read
+      if (!c.wait(&bars->ds_full, ph, 6)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      sum_ts(tmem + TM_DQ, tmem + TM_DS, 32, k_mn + (uint32_t)st * kTile16, n == 0);
+      tc_commit_warp(&bars->x_empty[st]);
+      if (n + 1 == here) tc_commit_warp(&bars->acc_done);
+      st = sn;
+    }
+  }
+}
+
+__device__ __forceinline__ void queries_proxy(const Pass& c) {
+  const AttnBwdArgs& p = *c.p;
+  Bars* bars = c.bars;
+  Ring<kRingK> x;
+  Ring<kRingV> y;
+  uint32_t g = 0;
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    const int id = c.unit(k);
+    if (id < 0) break;
+    const int b = id / c.n_tiles / p.n_heads;
+    const int count = c.walked(b);
+    const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + (size_t)b * p.seq : nullptr;
+    for (int n = 0; n < count; ++n, ++g, x.next(), y.next()) {
+      // K of tile g, clean: an arrival of phase g - 1 of s_read (phase g - 2 complete)
+      uint32_t bad[4] = {0, 0, 0, 0};
+      if (mask != nullptr) masked_keys(mask, c.tile(b, n) * BT, p.seq, c.lane, bad);
+      if ((g > 1 && !c.wait(&bars->s_read, g & 1u, 7)) || !c.wait(&bars->x_full[x.st], x.ph, 7)) {
+        ok = false;
+        break;
+      }
+      zero_rows(c.smem + OFF_K + x.st * TILE_BYTES, bad, c.lane);
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive(g == 0 ? &bars->first : &bars->s_read);
+      if (g == 0) continue;
+      // V of tile g (and dO, for a new unit)
+      if ((g > 1 && !c.wait(&bars->dp_read, g & 1u, 8)) || (n == 0 && !c.wait(&bars->own_y, (uint32_t)(k & 1), 8)) ||
+          !c.wait(&bars->y_full[y.st], y.ph, 8)) {
+        ok = false;
+        break;
+      }
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive(&bars->dp_read);
+    }
+  }
+}
+
+// Each warpgroup stores its half of the columns of dQ.
+__device__ __forceinline__ void queries_store(const Pass& c, const CUtensorMap& tmDQ, int id, int half, uint32_t t_row) {
+  const AttnBwdArgs& p = *c.p;
+  const int row = (id % c.n_tiles) * BT + (c.warp & 3) * 32;
+  uint8_t* out = c.smem + OFF_OUT + (c.warp - 4) * 4096;
+  if (c.lane == 0) bulk_wait_read();
+  __syncwarp();
+  stage64(out, t_row + TM_DQ + (uint32_t)half * 64u, p.scale, c.lane);
+  if (c.lane == 0 && row < p.seq) {
+    tma_store_3d(&tmDQ, out, half * 64, row, id / c.n_tiles);
+    bulk_commit();
+  }
+}
+
+__device__ __forceinline__ void queries_compute(const Pass& c, const CUtensorMap& tmDQ) {
+  const AttnBwdArgs& p = *c.p;
+  Bars* bars = c.bars;
+  const int half = (c.warp - 4) >> 2;          // key half of this warpgroup
+  const int r = (c.warp & 3) * 32 + c.lane;    // TMEM lane: query of the tile
+  const uint32_t t_row = c.tmem + ((uint32_t)((c.warp & 3) * 32) << 16);
+  const uint32_t t_s = t_row + TM_S + (uint32_t)half * 64u, t_dp = t_row + TM_DP + (uint32_t)half * 64u;
+  const uint32_t t_ds = t_row + TM_DS + (uint32_t)half * 32u, t_q = t_row + TM_Q + (uint32_t)half * 32u;
+  const f32x2_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2);
+  // a unit's row: its half of Q goes to TMEM (element d in column d / 2, as in memory)
+  uint32_t q[32];
+  float nl = 0.0f, nd = 0.0f;
+  auto read_row = [&](int id) {
+    const int row = (id % c.n_tiles) * BT + r, bh = id / c.n_tiles;
+    const uint4* src = reinterpret_cast<const uint4*>(p.qp + ((size_t)bh * p.seq + (row < p.seq ? row : 0)) * kHeadDim + half * 64);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = row < p.seq ? src[i] : make_uint4(0, 0, 0, 0);
+      q[4 * i] = v.x;
+      q[4 * i + 1] = v.y;
+      q[4 * i + 2] = v.z;
+      q[4 * i + 3] = v.w;
+    }
+  };
+  auto read_stats = [&](int id) {
+    const size_t at = (size_t)(id / c.n_tiles) * p.seq_pad + (id % c.n_tiles) * BT + r;
+    nl = p.nlse2[at];
+    nd = p.ndelta[at];
+  };
+  bool ok = true;
+  uint32_t g = 0;
+  Ring<kRingK> last;  // stage and phase of the tile before
+  int before = -1;
+  int id = c.unit(0);
+  if (id >= 0) {
+    read_row(id);
+    read_stats(id);
+    tmem_st32(t_q, q);
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (c.lane == 0) mbar_arrive(&bars->own_x);
+  }
+  for (int k = 0; ok && id >= 0; ++k) {
+    const int b = id / c.n_tiles / p.n_heads;
+    const int count = c.walked(b);
+    const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + (size_t)b * p.seq : nullptr;
+    const f32x2_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+    int next_id = -1;
+    // may this lane's two keys of the tile be attended to (read a tile ahead)
+    bool key[2];
+    auto read_mask = [&](int t) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int kc = t * BT + half * 64 + w * 32 + c.lane;
+        key[w] = kc < p.seq && (mask == nullptr || mask[kc < p.seq ? kc : 0] != 0);
+      }
+    };
+    read_mask(c.tile(b, 0));
+    for (int n = 0; n < count; ++n, ++g) {
+      const uint32_t ph = g & 1u;
+      const bool turn = n + 1 == count;  // the next tile is a new unit's
+      const uint32_t valid[2] = {__ballot_sync(0xffffffffu, key[0]), __ballot_sync(0xffffffffu, key[1])};
+      if (turn) {
+        next_id = c.unit(k + 1);
+        if (next_id >= 0) read_row(next_id);
+        ok = next_id != -2;
+      } else {
+        read_mask(c.tile(b, n + 1));
+      }
+      if (!ok || !c.wait(&bars->s_full, ph, 10)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (turn && next_id >= 0) tmem_st32(t_q, q);  // the scores of this unit's last tile are done with Q
       uint32_t pr[64], dp[64], pk[32];
       tmem_ld32(t_s, pr);
       tmem_ld32(t_s + 32, pr + 32);
       tmem_ld_wait();
+      if (turn) tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->s_read);
+      if (c.lane == 0) mbar_arrive(&bars->s_read);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         float z0, z1;
@@ -614,7 +948,7 @@ __device__ __forceinline__ void queries_pass(const CUtensorMap& tmK, const CUten
         pr[2 * i] = __float_as_uint(ex2_approx(z0));
         pr[2 * i + 1] = __float_as_uint(ex2_approx(z1));
       }
-      if (!mbar_wait_warp(&bars->dp_full, ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 11)) {
+      if (!c.wait(&bars->dp_full, ph, 12)) {
         ok = false;
         break;
       }
@@ -624,7 +958,7 @@ __device__ __forceinline__ void queries_pass(const CUtensorMap& tmK, const CUten
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->dp_read);
+      if (c.lane == 0) mbar_arrive(&bars->dp_read);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         float z0, z1;
@@ -639,36 +973,70 @@ __device__ __forceinline__ void queries_pass(const CUtensorMap& tmK, const CUten
 #pragma unroll
       for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
       // dQ of the tile before has read its dS
-      if (n > 0) {
-        if (!mbar_wait_warp(&bars->x_empty[before.st], before.ph, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 9)) {
+      if (g > 0) {
+        if (!c.wait(&bars->x_empty[last.st], last.ph, 9)) {
           ok = false;
           break;
         }
-        before.next();
+        last.next();
         tc_fence_after();
       }
       tmem_st32(t_ds, pk);
       tmem_st_wait();
+      if (n == 0 && before >= 0) {
+        if (!c.wait(&bars->acc_done, (uint32_t)((k - 1) & 1), 11)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        queries_store(c, tmDQ, before, half, t_row);
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->ds_full);
+      if (c.lane == 0) mbar_arrive(&bars->ds_full);
     }
-    if (ok && n > 0) ok = mbar_wait_warp(&bars->acc_done, 0, abort_flag, err, DEV_TIMEOUT_ATTN_BWD + 12);
-    if (ok) {
-      tc_fence_after();
-      __nv_bfloat16* dst = p.dqp + ((size_t)bh * S + row) * kHeadDim + half * 64;
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c)
-        store32(dst + c * 32, t_row + TM_DQ + (uint32_t)(half * 64 + c * 32), p.scale, n > 0, row < S);
-      tc_fence_before();
+    if (!ok) break;
+    before = id;
+    if (next_id < 0) {
+      if (c.wait(&bars->acc_done, (uint32_t)(k & 1), 13)) {
+        tc_fence_after();
+        queries_store(c, tmDQ, id, half, t_row);
+      }
+      break;
     }
+    id = next_id;
+    read_stats(id);
   }
+  tc_fence_before();
+}
+
+__device__ __forceinline__ void init_bars(Bars* bars, bool keys) {
+  mbar_init(&bars->own_x, keys ? 1 : 8);
+  mbar_init(&bars->own_y, 1);
+  mbar_init(&bars->own_x_empty, 1);
+  mbar_init(&bars->own_y_empty, 1);
+  for (int i = 0; i < 3; ++i) {
+    mbar_init(&bars->x_full[i], 1);
+    mbar_init(&bars->x_empty[i], 1);
+  }
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&bars->y_full[i], 1);
+    mbar_init(&bars->y_empty[i], 1);
+  }
+  mbar_init(&bars->first, 1);
+  mbar_init(&bars->s_full, 1);
+  mbar_init(&bars->dp_full, 1);
+  // 8 compute warps, and the wait proxy where it adds the next tile's landing
+  mbar_init(&bars->s_read, 9);
+  mbar_init(&bars->dp_read, 9);
+  mbar_init(&bars->p_full, 9);
+  mbar_init(&bars->ds_full, keys ? 9 : 8);
+  mbar_init(&bars->acc_done, 1);
+  for (int i = 0; i < 4; ++i) mbar_init(&bars->unit_full[i], 1);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
-                    const AttnBwdArgs p) {
+    attn_bwd_kernel(const __grid_constant__ AttnBwdMaps m, const __grid_constant__ AttnBwdArgs p) {
   // The swizzled tiles need a base at a multiple of 1024 bytes, which the window of dynamic shared memory
   // of a kernel without static shared memory has (checked: a launch elsewhere would report, not compute).
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -676,82 +1044,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) atomicCAS(p.err, 0, DEV_TIMEOUT_ATTN_BWD);
     return;
   }
-  Bars* bars = reinterpret_cast<Bars*>(smem + OFF_BAR);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_tiles = p.seq_pad / BT;
-  const unsigned units = (unsigned)(p.batch * p.n_heads) * (unsigned)n_tiles;
-  const bool keys = blockIdx.x < units;
-  const unsigned unit = keys ? blockIdx.x : blockIdx.x - units;
-  const int own = (int)(unit % n_tiles), bh = (int)(unit / n_tiles);
+  Bars* bars = reinterpret_cast<Bars*>(smem + OFF_BAR);            // keys pass
+  Bars* bars_q = reinterpret_cast<Bars*>(smem + OFF_BAR + kBarBytes);
+  Pass c;
+  c.p = &p;
+  c.smem = smem;
+  c.bars = bars;
+  c.abort_flag = &bars->abort_flag;
+  c.n_tiles = p.seq_pad / BT;
+  c.warp = threadIdx.x >> 5;
+  c.lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(&bars->own_x, keys ? 1 : 8);
-    mbar_init(&bars->own_y, 1);
-    for (int i = 0; i < kRingX; ++i) {
-      mbar_init(&bars->x_full[i], 1);
-      mbar_init(&bars->y_full[i], 1);
-      mbar_init(&bars->x_empty[i], 1);
-      mbar_init(&bars->y_empty[i], 1);
-    }
-    mbar_init(&bars->first, 1);
-    mbar_init(&bars->s_full, 1);
-    mbar_init(&bars->dp_full, 1);
-    // 8 compute warps, and the wait proxy where it adds the next tile's landing
-    mbar_init(&bars->s_read, 9);
-    mbar_init(&bars->dp_read, 9);
-    mbar_init(&bars->p_full, 9);
-    mbar_init(&bars->ds_full, keys ? 9 : 8);
-    mbar_init(&bars->acc_done, 1);
+    init_bars(bars, true);
+    init_bars(bars_q, false);
     bars->abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&m.q);
+    tma_prefetch_desc(&m.k);
+    tma_prefetch_desc(&m.v);
+    tma_prefetch_desc(&m.d_o);
   }
-  if (warp == 1) {
+  if (c.warp == 1) {
     tmem_alloc(&bars->tmem_slot, TM_COLS);
     tmem_relinquish();
-  }
-  grid_dep_wait();
-  grid_dep_launch();
-  // With a mask: a tile of keys without a valid one has zero gradients (keys pass) and is not walked
-  // (queries pass).
-  const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + (size_t)(bh / p.n_heads) * p.seq : nullptr;
-  bool walk = true;
-  if (keys && mask != nullptr) {
-    const int key = own * BT + (int)threadIdx.x;
-    walk = __syncthreads_or(threadIdx.x < BT && key < p.seq && mask[key < p.seq ? key : 0] != 0) != 0;
-  } else if (mask != nullptr) {
-    uint32_t* tile_any = reinterpret_cast<uint32_t*>(smem + OFF_STAT);
-    for (int i = threadIdx.x; i < (n_tiles + 31) / 32; i += kThreads) tile_any[i] = 0;
-    __syncthreads();
-    for (int t = warp; t < n_tiles; t += kThreads / 32) {
-      bool any = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int kc = t * BT + i * 32 + lane;
-        any |= kc < p.seq && mask[kc < p.seq ? kc : 0] != 0;
-      }
-      if (__any_sync(0xffffffffu, any) && lane == 0) atomicOr(&tile_any[t >> 5], 1u << (t & 31));
-    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem_slot;
-  if (keys) {
-    keys_pass(tmQ, tmK, tmV, tmDO, p, smem, bars, tmem, own, bh, walk ? n_tiles : 0);
+  c.tmem = bars->tmem_slot;
+  grid_dep_wait();
+  grid_dep_launch();
+  // Between the passes every role is done with the keys pass: its tiles and accumulators are free.
+  const bool keys = (long long)blockIdx.x < (long long)p.batch * p.n_heads * c.n_tiles;
+  if (c.warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (keys) {
+      if (c.warp == 0) keys_producer(c, m.q, m.k, m.v, m.d_o);
+      if (c.warp == 1) {
+        keys_mma(c);
+        tc_commit_warp(&bars->first);  // (unused in this pass) every MMA has completed
+        mbar_wait_drain(&bars->first, 0, p.err, DEV_TIMEOUT_ATTN_BWD + 14);
+      }
+      if (c.warp == 2) keys_proxy(c);
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+    }
+    c.bars = bars_q;
+    if (c.warp == 0) queries_producer(c, m.k, m.v, m.d_o);
+    if (c.warp == 1) {
+      queries_mma(c);
+      tc_commit_warp(&bars_q->own_x_empty);  // (unused in this pass)
+      mbar_wait_drain(&bars_q->own_x_empty, 0, p.err, DEV_TIMEOUT_ATTN_BWD + 14);
+    }
+    if (c.warp == 2) queries_proxy(c);
   } else {
-    queries_pass(tmK, tmV, tmDO, p, smem, bars, tmem, own, bh, n_tiles);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
+    if (keys) {
+      keys_compute(c);
+      __syncthreads();
+      tc_fence_after();
+    }
+    c.bars = bars_q;
+    queries_compute(c, m.dq);
+    if (c.lane == 0) bulk_wait();  // the outputs are in memory
   }
   __syncthreads();
-  if (warp == 1) {
+  if (c.warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, TM_COLS);
+    tmem_dealloc(c.tmem, TM_COLS);
   }
 }
 
 }  // namespace
 
-cudaError_t attention_bwd_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                 const CUtensorMap& tdo, const AttnBwdArgs& a, cudaStream_t s) {
+size_t attention_bwd_plan(AttnBwdArgs* a, uint8_t* base) {
+  a->seq_pad = (a->seq + BT - 1) / BT * BT;
+  const size_t rows = (size_t)a->batch * a->n_heads * a->seq_pad;
+  const auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+  size_t at = 0;
+  a->nlse2 = reinterpret_cast<float*>(base + at);
+  at += up(rows * sizeof(float));
+  a->ndelta = reinterpret_cast<float*>(base + at);
+  at += up(rows * sizeof(float));
+  a->counters = reinterpret_cast<int*>(base + at);
+  at += 256;
+  a->n_listed = reinterpret_cast<int*>(base + at);
+  at += up((size_t)a->batch * sizeof(int));
+  a->tiles = reinterpret_cast<int*>(base + at);
+  at += up((size_t)a->batch * (a->seq_pad / BT) * sizeof(int));
+  return at;
+}
+
+cudaError_t attention_bwd_launch(const AttnBwdMaps& m, const AttnBwdArgs& a, int num_sms, cudaStream_t s) {
   static bool attr_done[kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -767,10 +1153,12 @@ cudaError_t attention_bwd_launch(const CUtensorMap& tq, const CUtensorMap& tk, c
     attr_done[dev] = true;
   }
   const long long rows = (long long)a.batch * a.n_heads * a.seq_pad;
-  e = launch_kernel(attn_bwd_rows_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s, true, a);
+  const long long units = rows / BT;
+  e = launch_kernel(attn_bwd_rows_kernel, dim3((unsigned)((rows + 15) / 16 + (a.key_mask != nullptr ? a.batch : 0))),
+                    dim3(256), 0, s, true, a);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attn_bwd_kernel, dim3((unsigned)(2 * rows / BT)), dim3(kThreads), SMEM_TOTAL, s, true, tq, tk, tv,
-                       tdo, a);
+  return launch_kernel(attn_bwd_kernel, dim3((unsigned)(2 * units < num_sms ? 2 * units : num_sms)), dim3(kThreads), SMEM_TOTAL,
+                       s, true, m, a);
 }
 
 }  // namespace mi

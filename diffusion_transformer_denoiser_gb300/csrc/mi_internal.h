@@ -90,19 +90,29 @@ struct AttnBwdArgs {
   const __nv_bfloat16* o;      // [B, S, n_heads * 128], as the forward wrote it
   const __nv_bfloat16* d_o;    // [B, S, n_heads * 128]
   const float* lse;            // [B, n_heads, S]
-  float* nlse2;                // [B * n_heads, seq_pad]: -lse in base 2, -inf for an empty or missing row
-  float* ndelta;               // [B * n_heads, seq_pad]: -sum_d d_o o of the row
   __nv_bfloat16* dqp;          // [B, n_heads, S, 128]
   __nv_bfloat16* dkp;
   __nv_bfloat16* dv;           // v columns of row 0 of dqkv; rows 3 * n_heads * 128 apart
   float scale;                 // 1 / sqrt(128)
   float scale_log2;            // log2(e) / sqrt(128)
   int* err;
+  // Workspace (attention_bwd_plan): nothing in it outlives the call.
+  float* nlse2;                // [B * n_heads, seq_pad]: -lse in base 2, -inf for an empty or missing row
+  float* ndelta;               // [B * n_heads, seq_pad]: -sum_d d_o o of the row
+  int* counters;               // [2] units taken of the keys and the queries pass
+  int* n_listed;               // [B] key tiles with a valid key (with a key mask)
+  int* tiles;                  // [B, seq_pad / 128] which
 };
 
-// q, k maps as for the forward; v: 4-D over (128, n_heads, S, B) of the qkv buffer; d_o: the same over d_o.
-cudaError_t attention_bwd_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                 const CUtensorMap& tdo, const AttnBwdArgs& a, cudaStream_t s);
+// q, k: 3-D maps as for the forward; v, d_o: 4-D over (128, n_heads, S, B) of the qkv buffer's v columns and of
+// d_o, boxes of 128 rows.  dq: like q, boxes of 32 rows.
+struct AttnBwdMaps {
+  CUtensorMap q, k, v, d_o, dq;
+};
+
+// Lays the workspace out: fills in the workspace pointers of a (from base; none may be read) and returns its bytes.
+size_t attention_bwd_plan(AttnBwdArgs* a, uint8_t* base);
+cudaError_t attention_bwd_launch(const AttnBwdMaps& m, const AttnBwdArgs& a, int num_sms, cudaStream_t s);
 
 // Gradient of the q/k RMSNorm + rotary (elementwise.cu).  partial: [qk_norm_rope_bwd_grid()][256] floats.
 cudaError_t qk_norm_rope_bwd_launch(const __nv_bfloat16* qkv, const __nv_bfloat16* wq, const __nv_bfloat16* wk,
