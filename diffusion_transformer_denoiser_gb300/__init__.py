@@ -138,8 +138,8 @@ def _check(status: int):
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle: building a Stream object costs as much as a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -155,10 +155,11 @@ def _ptr(t: Optional[torch.Tensor], dtype=None) -> Optional[int]:
     return t.data_ptr()
 
 
-def _sized(t: Optional[torch.Tensor], n: int, name: str):
-    """The library sees pointers only: a tensor with too few or too many elements is refused here."""
-    if t is not None and t.numel() != n:
+def _sized(t: torch.Tensor, dtype, n: int, name: str) -> int:
+    """_ptr of a tensor of n elements: the library sees pointers only, so a wrong size is refused here."""
+    if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    return _ptr(t, dtype)
 
 
 _BF = torch.bfloat16
@@ -329,10 +330,9 @@ def rope_axes_tables(positions, axis_pairs, rope_cos, rope_sin, theta=10000.0, s
     if positions.dim() != 2 or positions.shape[1] != len(axis_pairs):
         raise ValueError(f"positions {tuple(positions.shape)} must be [rows, {len(axis_pairs)}], one column per axis")
     rows, n = positions.shape
-    _sized(rope_cos, rows * 64, "rope_cos")
-    _sized(rope_sin, rows * 64, "rope_sin")
     _check(lib().mi_rope_axes_tables(_ptr(positions, torch.float32), rows, n, (_I * n)(*axis_pairs), theta,
-                                     _ptr(rope_cos, torch.float32), _ptr(rope_sin, torch.float32), _stream(stream)))
+                                     _sized(rope_cos, torch.float32, rows * 64, "rope_cos"),
+                                     _sized(rope_sin, torch.float32, rows * 64, "rope_sin"), _stream(stream)))
 
 
 def time_advance(t, dt, stream=None):
@@ -399,22 +399,15 @@ def attention(qp, kp, qkv, key_mask, o, batch, seq, n_heads, stream=None, ws=Non
 
 
 # ------------------------------------------------------------------------------- training pass
-def _train_sizes(batch, seq, n_heads, **tensors):
-    """Element counts of the training pass's tensors, by the suffix-free names of the calls' arguments."""
-    packed = batch * n_heads * seq * 128
-    sizes = {"qkv": 3 * packed, "dqkv": 3 * packed, "lse": batch * n_heads * seq, "key_mask": batch * seq}
-    for name, t in tensors.items():
-        _sized(t, sizes.get(name, packed), name)
-
-
 def attention_lse(qp, kp, qkv, key_mask, o, lse, batch, seq, n_heads, ws=None, stream=None):
     """attention that also stores lse [batch, heads, seq] (fp32) for attention_backward; `ws` as for attention."""
-    _train_sizes(batch, seq, n_heads, qp=qp, kp=kp, qkv=qkv, key_mask=key_mask, o=o, lse=lse)
-    use_ws = ws is not None and ws.numel() > 0
-    _check(lib().mi_attention_lse(_ptr(qp, _BF), _ptr(kp, _BF), _ptr(qkv, _BF), _ptr(key_mask, torch.uint8), _ptr(o, _BF),
-                                  _ptr(lse, torch.float32), batch, seq, n_heads,
-                                  _ptr(ws, torch.uint8) if use_ws else None, ws.numel() if use_ws else 0,
-                                  _stream(stream)))
+    rows = batch * n_heads * seq
+    n = rows * 128
+    ws_bytes = 0 if ws is None else ws.numel()
+    _check(lib().mi_attention_lse(_sized(qp, _BF, n, "qp"), _sized(kp, _BF, n, "kp"), _sized(qkv, _BF, 3 * n, "qkv"),
+                                  None if key_mask is None else _sized(key_mask, torch.uint8, batch * seq, "key_mask"),
+                                  _sized(o, _BF, n, "o"), _sized(lse, torch.float32, rows, "lse"), batch, seq, n_heads,
+                                  _ptr(ws, torch.uint8) if ws_bytes else None, ws_bytes, _stream(stream)))
 
 
 def attention_backward_workspace_size(batch, seq, n_heads) -> int:
@@ -425,12 +418,14 @@ def attention_backward_workspace_size(batch, seq, n_heads) -> int:
 
 def attention_backward(qp, kp, qkv, key_mask, o, lse, d_o, dqp, dkp, dqkv, batch, seq, n_heads, ws, stream=None):
     """Gradients of attention_lse: dqp, dkp, and dv in the v columns of dqkv (its q and k columns are left alone)."""
-    _train_sizes(batch, seq, n_heads, qp=qp, kp=kp, qkv=qkv, key_mask=key_mask, o=o, lse=lse, d_o=d_o, dqp=dqp, dkp=dkp,
-                 dqkv=dqkv)
-    _check(lib().mi_attention_backward(_ptr(qp, _BF), _ptr(kp, _BF), _ptr(qkv, _BF), _ptr(key_mask, torch.uint8),
-                                       _ptr(o, _BF), _ptr(lse, torch.float32), _ptr(d_o, _BF), _ptr(dqp, _BF),
-                                       _ptr(dkp, _BF), _ptr(dqkv, _BF), batch, seq, n_heads, _ptr(ws, torch.uint8),
-                                       ws.numel(), _stream(stream)))
+    rows = batch * n_heads * seq
+    n = rows * 128
+    _check(lib().mi_attention_backward(
+        _sized(qp, _BF, n, "qp"), _sized(kp, _BF, n, "kp"), _sized(qkv, _BF, 3 * n, "qkv"),
+        None if key_mask is None else _sized(key_mask, torch.uint8, batch * seq, "key_mask"), _sized(o, _BF, n, "o"),
+        _sized(lse, torch.float32, rows, "lse"), _sized(d_o, _BF, n, "d_o"), _sized(dqp, _BF, n, "dqp"),
+        _sized(dkp, _BF, n, "dkp"), _sized(dqkv, _BF, 3 * n, "dqkv"), batch, seq, n_heads, _ptr(ws, torch.uint8),
+        ws.numel(), _stream(stream)))
 
 
 def qk_norm_rope_backward_workspace_size(batch, seq, n_heads) -> int:
@@ -442,17 +437,18 @@ def qk_norm_rope_backward_workspace_size(batch, seq, n_heads) -> int:
 def qk_norm_rope_backward(qkv, q_norm_w, k_norm_w, rope_cos, rope_sin, dqp, dkp, dqkv, dq_norm_w, dk_norm_w, batch, seq,
                           n_heads, ws, eps=1e-6, rope_bstride=0, stream=None):
     """Gradients of qk_norm_rope: the q and k columns of dqkv (its v columns are left alone) and the two gains' (fp32)."""
-    _train_sizes(batch, seq, n_heads, qkv=qkv, dqp=dqp, dkp=dkp, dqkv=dqkv)
-    for name, t in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w), ("dq_norm_w", dq_norm_w), ("dk_norm_w", dk_norm_w)):
-        _sized(t, 128, name)
-    for name, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)):
-        if t.numel() < (batch - 1) * rope_bstride + seq * 64:
-            raise ValueError(f"{name} has {t.numel()} elements, too few for {batch} tables {rope_bstride} apart")
-    _check(lib().mi_qk_norm_rope_backward(_ptr(qkv, _BF), _ptr(q_norm_w, _BF), _ptr(k_norm_w, _BF),
-                                          _ptr(rope_cos, torch.float32), _ptr(rope_sin, torch.float32), rope_bstride,
-                                          _ptr(dqp, _BF), _ptr(dkp, _BF), _ptr(dqkv, _BF),
-                                          _ptr(dq_norm_w, torch.float32), _ptr(dk_norm_w, torch.float32), batch, seq,
-                                          n_heads, eps, _ptr(ws, torch.uint8), ws.numel(), _stream(stream)))
+    n = batch * n_heads * seq * 128
+    table = (batch - 1) * rope_bstride + seq * 64
+    if rope_cos.numel() < table or rope_sin.numel() < table:
+        raise ValueError(f"rope_cos, rope_sin have {rope_cos.numel()}, {rope_sin.numel()} elements, too few for {batch} "
+                         f"tables of {seq} rows, {rope_bstride} apart")
+    f32 = torch.float32
+    _check(lib().mi_qk_norm_rope_backward(
+        _sized(qkv, _BF, 3 * n, "qkv"), _sized(q_norm_w, _BF, 128, "q_norm_w"), _sized(k_norm_w, _BF, 128, "k_norm_w"),
+        _ptr(rope_cos, f32), _ptr(rope_sin, f32), rope_bstride, _sized(dqp, _BF, n, "dqp"), _sized(dkp, _BF, n, "dkp"),
+        _sized(dqkv, _BF, 3 * n, "dqkv"), _sized(dq_norm_w, f32, 128, "dq_norm_w"),
+        _sized(dk_norm_w, f32, 128, "dk_norm_w"), batch, seq, n_heads, eps, _ptr(ws, torch.uint8), ws.numel(),
+        _stream(stream)))
 
 
 def gated_add(x, y, mod, gate_row, out, batch, seq, stream=None):

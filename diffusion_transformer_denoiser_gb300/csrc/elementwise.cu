@@ -274,91 +274,142 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __nv_bfloat16* 
 // ------------------------------------------------------------------------------------ q/k gradient
 // With n = x r, r = rsqrt(mean x^2 + eps), y = rotate(n gain): the gradient of y is rotated back (dz),
 // dgain = sum of dz n over all rows and heads, and with t = dz gain, dx = r (t - n mean(t n)).
-// One warp per (row, head) as in the forward: lanes 0-15 q, lanes 16-31 k.  Each CTA sums its share of
-// dgain in registers and adds its warps' sums in a fixed order; a second kernel adds the CTAs' sums.
+// HBM bound: 12 bytes per element of q and k (8260 rows x 24 heads: 52 us, 5.88 TB/s; with 2 CTAs per SM
+// 59 us, with 2 heads at a time and 4 CTAs 58, and 3 heads 56).  A warp takes kQkHeads heads of a row at a time (lanes 0-15 q,
+// lanes 16-31 k, 8 elements each), with all their loads in flight before the first is used, and one read
+// of the row's angles for all of them.  dgain is summed in registers, then over the CTA's warps, then over
+// the CTAs, each in a fixed order: by a second kernel, or (kCluster, few rows) over the one cluster of the
+// launch through shared memory, which saves the second launch where launches are what a call costs.
 constexpr int kQkBwdThreads = 256;
+constexpr int kQkBwdWarps = kQkBwdThreads / 32;
+constexpr int kQkHeads = 4;
+constexpr int kQkCtas = 3;  // per SM
+constexpr int kQkCluster = 8;
 
-__global__ void __launch_bounds__(kQkBwdThreads)
+template <bool kCluster>
+__global__ void __launch_bounds__(kQkBwdThreads, kQkCtas)
     qk_norm_rope_bwd_kernel(const __nv_bfloat16* __restrict__ qkv, const __nv_bfloat16* __restrict__ wq,
                             const __nv_bfloat16* __restrict__ wk, const float* __restrict__ cosv,
                             const float* __restrict__ sinv, int rope_bstride, const __nv_bfloat16* __restrict__ dqp,
                             const __nv_bfloat16* __restrict__ dkp, __nv_bfloat16* __restrict__ dqkv,
-                            float* __restrict__ partial, int batch, int seq, int heads, float eps) {
-  __shared__ float sums[kQkBwdThreads / 32][256];
+                            float* __restrict__ partial, float* __restrict__ dwq, float* __restrict__ dwk, int batch,
+                            int seq, int heads, float eps) {
+  __shared__ float sums[kQkBwdWarps][256];
+  __shared__ float cta_sum[256];
   grid_dep_wait();
+  grid_dep_launch();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int which = lane >> 4;  // 0: q, 1: k
   const int e0 = (lane & 15) * 8;
   const int H = heads * kHeadDim;
-  const long long total = (long long)batch * seq * heads;
-  const long long stride = (long long)gridDim.x * (kQkBwdThreads / 32);
+  const int groups = (heads + kQkHeads - 1) / kQkHeads;
+  const long long total = (long long)batch * seq * groups;
+  const long long stride = (long long)gridDim.x * kQkBwdWarps;
   float g[8], dg[8];
   unpack8(__ldg(reinterpret_cast<const uint4*>((which ? wk : wq) + e0)), g);
 #pragma unroll
   for (int e = 0; e < 8; ++e) dg[e] = 0.0f;
-  for (long long item = (long long)blockIdx.x * (kQkBwdThreads / 32) + warp; item < total; item += stride) {
-    const int h = (int)(item % heads);
-    const long long row = item / heads;
+  for (long long item = (long long)blockIdx.x * kQkBwdWarps + warp; item < total; item += stride) {
+    const int h0 = (int)(item % groups) * kQkHeads;
+    const long long row = item / groups;
     const int b = (int)(row / seq);
     const int s = (int)(row % seq);
-    const size_t at = (size_t)row * 3 * H + (size_t)which * H + (size_t)h * kHeadDim + e0;
-    const uint4 xv = *reinterpret_cast<const uint4*>(qkv + at);
-    const uint4 yv = *reinterpret_cast<const uint4*>((which ? dkp : dqp) + (((size_t)b * heads + h) * seq + s) * kHeadDim + e0);
+    const size_t x_at = (size_t)row * 3 * H + (size_t)which * H + (size_t)h0 * kHeadDim + e0;
+    const __nv_bfloat16* dy = (which ? dkp : dqp) + (((size_t)b * heads + h0) * seq + s) * kHeadDim + e0;
+    uint4 xv[kQkHeads], yv[kQkHeads];
+#pragma unroll
+    for (int i = 0; i < kQkHeads; ++i) {
+      if (h0 + i < heads) {
+        xv[i] = __ldg(reinterpret_cast<const uint4*>(qkv + x_at + (size_t)i * kHeadDim));
+        yv[i] = __ldg(reinterpret_cast<const uint4*>(dy + (size_t)i * seq * kHeadDim));
+      } else {
+        xv[i] = yv[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
     const size_t tab = (size_t)b * rope_bstride + (size_t)s * (kHeadDim / 2) + (lane & 15) * 4;
     const float4 c4 = __ldg(reinterpret_cast<const float4*>(cosv + tab));
     const float4 s4 = __ldg(reinterpret_cast<const float4*>(sinv + tab));
     const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
-    float x[8], y[8];
-    unpack8(xv, x);
-    unpack8(yv, y);
 #pragma unroll
-    for (int pr = 0; pr < 4; ++pr) {
-      const float a = y[2 * pr], bb = y[2 * pr + 1];
-      y[2 * pr] = fmaf(a, cs[pr], bb * sn[pr]);
-      y[2 * pr + 1] = fmaf(bb, cs[pr], -a * sn[pr]);
-    }
-    float ss = 0.0f, tx = 0.0f;  // sums of x^2 and of t x
+    for (int i = 0; i < kQkHeads; ++i) {
+      float x[8], y[8];
+      unpack8(xv[i], x);
+      unpack8(yv[i], y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      ss = fmaf(x[e], x[e], ss);
-      tx = fmaf(y[e] * g[e], x[e], tx);
-    }
+      for (int pr = 0; pr < 4; ++pr) {
+        const float a = y[2 * pr], bb = y[2 * pr + 1];
+        y[2 * pr] = fmaf(a, cs[pr], bb * sn[pr]);
+        y[2 * pr + 1] = fmaf(bb, cs[pr], -a * sn[pr]);
+      }
+      float ss = 0.0f, tx = 0.0f;  // sums of x^2 and of t x
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      tx += __shfl_xor_sync(0xffffffffu, tx, o);
-    }
-    const float r = rsqrtf(ss * (1.0f / kHeadDim) + eps);
-    const float m = tx * r * r * (1.0f / kHeadDim);  // mean(t n) r
-    float o[8];
+      for (int e = 0; e < 8; ++e) {
+        ss = fmaf(x[e], x[e], ss);
+        tx = fmaf(y[e] * g[e], x[e], tx);
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dg[e] = fmaf(y[e], x[e] * r, dg[e]);
-      o[e] = r * fmaf(y[e], g[e], -x[e] * m);
+      for (int o = 8; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        tx += __shfl_xor_sync(0xffffffffu, tx, o);
+      }
+      const float r = rsqrtf(ss * (1.0f / kHeadDim) + eps);
+      const float m = tx * r * r * (1.0f / kHeadDim);  // mean(t n) r
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dg[e] = fmaf(y[e], x[e] * r, dg[e]);
+        o[e] = r * fmaf(y[e], g[e], -x[e] * m);
+      }
+      if (h0 + i < heads) *reinterpret_cast<uint4*>(dqkv + x_at + (size_t)i * kHeadDim) = pack8(o);
     }
-    *reinterpret_cast<uint4*>(dqkv + at) = pack8(o);
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) sums[warp][which * 128 + e0 + e] = dg[e];
   __syncthreads();
   float t = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kQkBwdThreads / 32; ++w) t += sums[w][threadIdx.x];
-  partial[(size_t)blockIdx.x * 256 + threadIdx.x] = t;
+  for (int w = 0; w < kQkBwdWarps; ++w) t += sums[w][threadIdx.x];
+  if (!kCluster) {
+    partial[(size_t)blockIdx.x * 256 + threadIdx.x] = t;
+  } else {
+    cta_sum[threadIdx.x] = t;
+    cluster_sync();
+    constexpr int kCols = 256 / kQkCluster;  // columns of this CTA
+    if (threadIdx.x < kCols) {
+      const int c = (int)cluster_rank() * kCols + (int)threadIdx.x;
+      float v[kQkCluster];
+#pragma unroll
+      for (int i = 0; i < kQkCluster; ++i)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[i]) : "r"(cluster_addr(&cta_sum[c], (uint32_t)i)) : "memory");
+      float all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kQkCluster; ++i) all += v[i];
+      (c < 128 ? dwq : dwk)[c & 127] = all;
+    }
+    cluster_sync();  // nobody leaves while its sums are being read
+  }
 }
 
-// dgain[c] = sum of the CTAs' partial sums; four groups of threads take every fourth CTA each.
-__global__ void __launch_bounds__(1024) qk_gain_sum_kernel(const float* __restrict__ partial, int n,
-                                                           float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ float sums[4][256];
+// dgain[c] = sum of the CTAs' partial sums: a block takes 16 of the 256 columns, 16 groups of threads every
+// 16th CTA each, and adds the groups in order.
+__global__ void __launch_bounds__(256) qk_gain_sum_kernel(const float* __restrict__ partial, int n,
+                                                          float* __restrict__ dwq, float* __restrict__ dwk) {
+  __shared__ float sums[16][17];
   grid_dep_wait();
-  const int c = threadIdx.x & 255, grp = threadIdx.x >> 8;
+  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + col;
   float t = 0.0f;
-  for (int i = grp; i < n; i += 4) t += partial[(size_t)i * 256 + c];
-  sums[grp][c] = t;
+#pragma unroll 8
+  for (int i = grp; i < n; i += 16) t += partial[(size_t)i * 256 + c];
+  sums[grp][col] = t;
   __syncthreads();
-  if (grp == 0) (c < 128 ? dwq : dwk)[c & 127] = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+  if (grp == 0) {
+    float all = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) all += sums[i][col];
+    (c < 128 ? dwq : dwk)[c & 127] = all;
+  }
 }
 
 // ------------------------------------------------------------------------------------ gated add
@@ -469,39 +520,61 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float* __restrict__ cos
 }
 
 // Rotary tables from per-token positions: pair j of row r turns by pos[r, axis j] (hi_j + lo_j) full
-// turns, hi + lo a frequency over 2 pi in 48 bits.  The product is formed in fp32 pairs (its rounding
-// recovered by one fma), whole quarter turns are taken off exactly, and the sine and cosine see at
-// most an eighth of a turn: the angle is as exact as in 64 bits up to positions of 2^24.  16 lanes take
-// a row, 4 pairs each, and keep their frequencies in registers over the rows of a grid-stride loop.
+// turns, hi + lo a frequency over 2 pi in 48 bits.  The product is formed in two fp32 parts (t, and what its
+// rounding and lo leave: recovered by two fmas), whole and quarter turns are taken off t exactly, and the
+// Taylor polynomials of sine and cosine see at most an eighth of a turn, where their first terms left out
+// are below 2^-28: the angle is as exact as in 64 bits up to positions of 2^24.  The rest of a far position
+// may itself be turns; taking those off keeps every entry a sine or cosine of some angle.
+// 16 lanes take a row, 4 pairs each, and keep their frequencies in registers over the rows of a
+// grid-stride loop (a warp's 16 different constants are read one by one: few CTAs, vector loads).
 __global__ void __launch_bounds__(256) rope_axes_kernel(const float* __restrict__ pos, int rows, int n_axes,
                                                         const __grid_constant__ RopeAxes f, float* __restrict__ cosv,
                                                         float* __restrict__ sinv) {
   grid_dep_wait();
+  grid_dep_launch();
   const int j0 = (threadIdx.x & 15) * 4;
-  float hi[4], lo[4];
-  int axis[4];
+  const float4 hi4 = *reinterpret_cast<const float4*>(f.hi + j0), lo4 = *reinterpret_cast<const float4*>(f.lo + j0);
+  const uchar4 ax4 = *reinterpret_cast<const uchar4*>(f.axis + j0);
+  const float hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w}, lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w};
+  const int axis[4] = {ax4.x, ax4.y, ax4.z, ax4.w};
+  const long long stride = (long long)gridDim.x * 16;
+  long long r = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  float next[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto read = [&](long long row) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    hi[i] = f.hi[j0 + i];
-    lo[i] = f.lo[j0 + i];
-    axis[i] = f.axis[j0 + i];
-  }
-  const int stride = gridDim.x * 16;
-  for (long long r = blockIdx.x * 16 + (threadIdx.x >> 4); r < rows; r += stride) {
+    for (int i = 0; i < 4; ++i) next[i] = __ldg(pos + row * n_axes + axis[i]);
+  };
+  if (r < rows) read(r);
+  for (; r < rows; r += stride) {
+    const float at[4] = {next[0], next[1], next[2], next[3]};
+    if (r + stride < rows) read(r + stride);
     float c[4], s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float p = __ldg(pos + r * n_axes + axis[i]);
+      const float p = at[i];
       const float t = p * hi[i];
-      const float rest = fmaf(p, lo[i], fmaf(p, hi[i], -t));
-      const float n = rintf(4.0f * t);
-      const float turn = fmaf(n, -0.25f, t) + rest;
-      const int quarter = (int)(n - 4.0f * floorf(0.25f * n));
-      float sv, cv;
-      sincospif(2.0f * turn, &sv, &cv);
-      const float cq = (quarter & 1) ? sv : cv, sq = (quarter & 1) ? cv : sv;
-      c[i] = (quarter == 1 || quarter == 2) ? -cq : cq;
-      s[i] = (quarter >= 2) ? -sq : sq;
+      float rest = fmaf(p, lo[i], fmaf(p, hi[i], -t));
+      rest -= rintf(rest);
+      const float frac = t - rintf(t);
+      constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number in the low bits
+      const float nb = fmaf(frac + rest, 4.0f, kMagic);
+      const uint32_t quarter = __float_as_uint(nb);
+      const float x = (fmaf(nb - kMagic, -0.25f, frac) + rest) * 6.283185307179586f;
+      const float x2 = x * x;
+      float sp = fmaf(x2, 2.75573192e-6f, -1.98412698e-4f);   // 1/9!, -1/7!
+      sp = fmaf(x2, sp, 8.33333333e-3f);                      // 1/5!
+      sp = fmaf(x2, sp, -1.66666667e-1f);                     // -1/3!
+      const float sv = fmaf(x * x2, sp, x);
+      float cp = fmaf(x2, -2.75573192e-7f, 2.48015873e-5f);   // -1/10!, 1/8!
+      cp = fmaf(x2, cp, -1.38888889e-3f);                     // -1/6!
+      cp = fmaf(x2, cp, 4.16666667e-2f);                      // 1/4!
+      cp = fmaf(x2, cp, -0.5f);
+      const float cv = fmaf(x2, cp, 1.0f);
+      // a quarter turn on: (c, s) -> (-s, c)
+      const bool odd = quarter & 1u;
+      const uint32_t cq = __float_as_uint(odd ? sv : cv), sq = __float_as_uint(odd ? cv : sv);
+      c[i] = __uint_as_float(cq ^ (((quarter + 1u) & 2u) << 30));
+      s[i] = __uint_as_float(sq ^ ((quarter & 2u) << 30));
     }
     *reinterpret_cast<float4*>(cosv + r * 64 + j0) = make_float4(c[0], c[1], c[2], c[3]);
     *reinterpret_cast<float4*>(sinv + r * 64 + j0) = make_float4(s[0], s[1], s[2], s[3]);
@@ -595,9 +668,18 @@ cudaError_t qk_norm_rope_launch(const __nv_bfloat16* qkv, const __nv_bfloat16* w
   return cudaGetLastError();
 }
 
+static long long qk_bwd_items(int batch, int seq, int n_heads) {
+  return (long long)batch * seq * ((n_heads + kQkHeads - 1) / kQkHeads);
+}
+
+// One cluster for up to 2 turns of its 64 warps; beyond, the whole GPU and a second kernel.
+static bool qk_bwd_one_cluster(long long items) { return items <= 2LL * kQkCluster * kQkBwdWarps; }
+
 int qk_norm_rope_bwd_grid(int batch, int seq, int n_heads, int num_sms) {
-  const long long need = ((long long)batch * seq * n_heads + kQkBwdThreads / 32 - 1) / (kQkBwdThreads / 32);
-  const long long cap = 4LL * num_sms;
+  const long long items = qk_bwd_items(batch, seq, n_heads);
+  if (qk_bwd_one_cluster(items)) return kQkCluster;
+  const long long need = (items + kQkBwdWarps - 1) / kQkBwdWarps;
+  const long long cap = (long long)kQkCtas * num_sms;
   return (int)(need < cap ? need : cap);
 }
 
@@ -607,10 +689,13 @@ cudaError_t qk_norm_rope_bwd_launch(const __nv_bfloat16* qkv, const __nv_bfloat1
                                     float* partial, int batch, int seq, int n_heads, float eps, int num_sms,
                                     cudaStream_t s) {
   const int grid = qk_norm_rope_bwd_grid(batch, seq, n_heads, num_sms);
-  cudaError_t e = launch_kernel(qk_norm_rope_bwd_kernel, dim3(grid), dim3(kQkBwdThreads), 0, s, true, qkv, wq, wk, cos, sin,
-                                rope_bstride, dqp, dkp, dqkv, partial, batch, seq, n_heads, eps);
+  if (qk_bwd_one_cluster(qk_bwd_items(batch, seq, n_heads)))
+    return launch_kernel_cluster(qk_norm_rope_bwd_kernel<true>, dim3(grid), dim3(kQkBwdThreads), kQkCluster, s, qkv, wq, wk,
+                                 cos, sin, rope_bstride, dqp, dkp, dqkv, partial, dwq, dwk, batch, seq, n_heads, eps);
+  cudaError_t e = launch_kernel(qk_norm_rope_bwd_kernel<false>, dim3(grid), dim3(kQkBwdThreads), 0, s, true, qkv, wq, wk,
+                                cos, sin, rope_bstride, dqp, dkp, dqkv, partial, dwq, dwk, batch, seq, n_heads, eps);
   if (e != cudaSuccess) return e;
-  return launch_kernel(qk_gain_sum_kernel, dim3(1), dim3(1024), 0, s, true, (const float*)partial, grid, dwq, dwk);
+  return launch_kernel(qk_gain_sum_kernel, dim3(16), dim3(256), 0, s, true, (const float*)partial, grid, dwq, dwk);
 }
 
 cudaError_t gated_add_launch(const __nv_bfloat16* x, const __nv_bfloat16* y, const __nv_bfloat16* gate,
@@ -664,7 +749,7 @@ cudaError_t rope_table_launch(float* cosv, float* sinv, int S, int text_pad, int
 cudaError_t rope_axes_launch(const float* pos, int rows, int n_axes, const RopeAxes& f, float* cosv, float* sinv,
                              int num_sms, cudaStream_t s) {
   const int need = (rows + 15) / 16;
-  const int cap = 8 * num_sms;
+  const int cap = 4 * num_sms;
   return launch_kernel(rope_axes_kernel, dim3(need < cap ? need : cap), dim3(256), 0, s, true, pos, rows, n_axes, f, cosv,
                        sinv);
 }

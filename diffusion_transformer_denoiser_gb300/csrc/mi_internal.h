@@ -125,7 +125,8 @@ int qk_norm_rope_bwd_grid(int batch, int seq, int n_heads, int num_sms);
 // Rotary tables of tokens with several position axes (elementwise.cu): pair j of a row turns by
 // pos[row, axis[j]] * (hi[j] + lo[j]) full turns.
 struct RopeAxes {
-  float hi[64], lo[64];
+  alignas(16) float hi[64];
+  float lo[64];
   unsigned char axis[64];
 };
 cudaError_t rope_axes_launch(const float* pos, int rows, int n_axes, const RopeAxes& f, float* cosv, float* sinv,
@@ -178,6 +179,26 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (pdl && pdl_enabled()) ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// The same for a kernel whose CTAs form clusters (no dynamic shared memory).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned cluster, cudaStream_t s,
+                                  Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 

@@ -137,11 +137,12 @@ def test_binding_refuses_wrong_sizes():
     t = torch.empty(10, 64)
     with pytest.raises(ValueError, match="one column per axis"):
         mi.rope_axes_tables(torch.empty(10, 2), (16, 24, 24), t, t)
-    with pytest.raises(ValueError, match="rope_cos"):
-        mi.rope_axes_tables(torch.empty(11, 2), (32, 32), t, t)
-    bf = torch.empty(1, 2, 5, 128, dtype=torch.bfloat16)
-    qkv = torch.empty(5, 768, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="lse"):
-        mi.attention_lse(bf, bf, qkv, None, bf, torch.empty(9), 1, 5, 2)
     with pytest.raises(ValueError, match="must live on the GPU"):
-        mi.attention_lse(bf, bf, qkv, None, bf, torch.empty(10), 1, 5, 2)
+        mi.rope_axes_tables(torch.empty(10, 2), (32, 32), t, t)
+    bf = torch.empty(1, 2, 5, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="qp has 1280 elements"):
+        mi.attention_lse(bf, bf, bf, None, bf, bf, 1, 6, 2)
+    with pytest.raises(ValueError, match="qp has 1280 elements"):
+        mi.attention_backward(bf, bf, bf, None, bf, bf, bf, bf, bf, bf, 1, 4, 2, bf)
+    with pytest.raises(ValueError, match="too few for 2 tables"):
+        mi.qk_norm_rope_backward(bf, bf, bf, t, t, bf, bf, bf, bf, bf, 2, 5, 2, bf, rope_bstride=640)
