@@ -346,6 +346,7 @@ static mi_status block_forward_impl(mi_block* blk, int batch, int S, const void*
     aa.part = at_part;
     aa.count = at_count;
     aa.lse = nullptr;
+    aa.list_ws = nullptr;
     e = mi::attention_launch(tq, tk, tv, aa, blk->num_sms, s);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   }
@@ -815,7 +816,9 @@ static mi_status attention_common(const void* qp, const void* kp, const void* qk
   DeviceInfo* dev = nullptr;
   mi_status st = require_sm103(&dev);
   if (st != MI_OK) return st;
-  const size_t need = use_ws ? mi::attention_scratch_bytes(batch, seq, n_heads, dev->num_sms) : 0;
+  const size_t scratch = use_ws ? mi::attention_scratch_bytes(batch, seq, n_heads, dev->num_sms) : 0;
+  const size_t list = scratch > 0 && lse != nullptr ? mi::attention_list_bytes(batch, seq, n_heads, dev->num_sms) : 0;
+  const size_t need = scratch + list;
   if (need > 0) {
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
       return fail(MI_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
@@ -841,12 +844,16 @@ static mi_status attention_common(const void* qp, const void* kp, const void* qk
   aa.part = nullptr;
   aa.count = nullptr;
   aa.lse = lse;
+  aa.list_ws = nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (need > 0) {
     const size_t cb_bytes = mi::attention_count_bytes(batch, seq, n_heads);
     aa.count = static_cast<int*>(ws);
     aa.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + cb_bytes);
-    cudaError_t e = cudaMemsetAsync(aa.count, 0, cb_bytes, s);
+    // the training forward's list of key tiles follows the partial results
+    if (lse != nullptr && key_mask != nullptr && list > 0) aa.list_ws = static_cast<uint8_t*>(ws) + scratch;
+    cudaError_t e = aa.list_ws != nullptr ? mi::attention_prepare_launch(aa, dev->num_sms, s)
+                                          : cudaMemsetAsync(aa.count, 0, cb_bytes, s);
     if (e != cudaSuccess) return cuda_fail(e, "attention counters");
   }
   cudaError_t e = mi::attention_launch(tq, tk, tv, aa, dev->num_sms, s);
@@ -865,6 +872,8 @@ mi_status mi_attention_workspace_size(int batch, int seq, int n_heads, size_t* b
   mi_status st = require_sm103(&dev);
   if (st != MI_OK) return st;
   *bytes = mi::attention_scratch_bytes(batch, seq, n_heads, dev->num_sms);
+  // mi_attention_lse with a mask keeps its list of key tiles behind that
+  if (*bytes > 0) *bytes += mi::attention_list_bytes(batch, seq, n_heads, dev->num_sms);
   return MI_OK;
 }
 

@@ -68,7 +68,11 @@ constexpr int OFF_MASK = OFF_V + 2 * TILE_BYTES;
 constexpr int kMaskWords = 2048;  // key-validity bitmask held in shared memory: up to 65536 keys
 constexpr int OFF_BAR = OFF_MASK + kMaskWords * 4;
 constexpr int OFF_SEG = OFF_BAR + 256;          // the CTA's segment list (int4 each) and its length
+// training forward with a mask on the split schedule: the elements' key tiles with a valid key
+constexpr int kListTiles = 4096, kListElements = 1280;
+constexpr int OFF_LIST = OFF_SEG + 16 * 16 + 16;
 constexpr int SMEM_TOTAL = OFF_SEG + 16 * 16 + 16 + 1024;
+constexpr int SMEM_TOTAL_LIST = OFF_LIST + kListTiles * 2 + 1024;
 
 constexpr uint32_t TM_S = 0;    // S_i at TM_S + 128 i (P_i in its first 64 columns)
 constexpr uint32_t TM_O = 256;  // O_i at TM_O + 128 i
@@ -107,6 +111,130 @@ __device__ int build_segments(int4* tab, long long total, int n_kv) {
   return n;
 }
 
+// The training forward with a mask, on the split schedule, leaves out key tiles without a valid key, so padding
+// costs nothing.  A kernel before it lists the tiles of every batch element that hold one (n_kv places each;
+// kListPartial marks a tile with masked keys, or one that ends the sequence inside it), cuts the listed work
+// into the CTAs' segments and clears the outputs of the elements without any.  A segment is {unit, first place
+// in the list, tiles, flags}: bit 0 of the flags for the first tiles of the unit, bit 1 for its last.  The shares
+// are equal as above when every unit spans at most two of them; else (few tiles left) the units with a
+// tile are dealt out whole.  (In the attention kernel itself the same work costs the loops their place in the
+// instruction cache: 167 against 156 us at 4130 rows x 24 heads.)
+constexpr int kSegFirst = 1, kSegLast = 2;
+constexpr int kListPartial = 0x8000;
+
+// In the workspace, behind the partial results.
+struct ListWorkspace {
+  int4* seg;         // [CTAs][kMaxSegs]
+  int* seg_count;    // [CTAs]
+  uint16_t* list;    // [batch][n_kv]
+};
+
+__host__ __device__ inline size_t list_workspace(uint8_t* base, int batch, int n_kv, int ctas, ListWorkspace* w) {
+  size_t at = 0;
+  w->seg = reinterpret_cast<int4*>(base + at);
+  at += (size_t)ctas * kMaxSegs * sizeof(int4);
+  w->seg_count = reinterpret_cast<int*>(base + at);
+  at += ((size_t)ctas * sizeof(int) + 15) & ~(size_t)15;
+  w->list = reinterpret_cast<uint16_t*>(base + at);
+  at += (size_t)batch * n_kv * sizeof(uint16_t);
+  return (at + 255) & ~(size_t)255;
+}
+
+__device__ int build_masked_segments(int4* tab, const uint16_t* listed, int n_kv, int batch, int per_element, int cta, int ctas) {
+  long long total = 0;
+  int most = 0, least = 0x7fffffff;
+  for (int b = 0; b < batch; ++b) {
+    const int cnt = listed[b];
+    total += (long long)per_element * cnt;
+    if (cnt > most) most = cnt;
+    if (cnt > 0 && cnt < least) least = cnt;
+  }
+  const long long share = total / ctas;
+  int n = 0;
+  if (share >= most && (share + 1) / least + 2 <= kMaxSegs) {
+    long long w = total * cta / ctas, at = 0;  // `at`: tiles of the elements before b
+    const long long w1 = total * (cta + 1) / ctas;
+    for (int b = 0; b < batch && w < w1; ++b) {
+      const int cnt = listed[b];
+      const long long end = at + (long long)per_element * cnt;
+      while (w < w1 && w < end && n < kMaxSegs) {
+        const int u = (int)((w - at) / cnt), jb = (int)((w - at) % cnt);
+        const int len = (long long)(cnt - jb) <= w1 - w ? cnt - jb : (int)(w1 - w);
+        tab[n++] = make_int4(b * per_element + u, b * n_kv + jb, len,
+                             (jb == 0 ? kSegFirst : 0) | (jb + len == cnt ? kSegLast : 0));
+        w += len;
+      }
+      at = end;
+    }
+  } else {
+    int ahead = cta;  // units with a tile still to pass before this CTA's next
+    for (int b = 0; b < batch; ++b) {
+      const int cnt = listed[b];
+      if (cnt == 0) continue;
+      for (; ahead < per_element && n < kMaxSegs; ahead += ctas)
+        tab[n++] = make_int4(b * per_element + ahead, b * n_kv, cnt, kSegFirst | kSegLast);
+      ahead -= per_element;
+    }
+  }
+  return n;
+}
+
+constexpr int kPrepareThreads = 1024;
+
+// Every block finds the tiles' flags (bit 0: a valid key, bit 1: one that is not) and the elements' counts;
+// block 0 writes the list and the segments, and all of them clear counters and empty elements' outputs.
+__global__ void __launch_bounds__(kPrepareThreads) attn_prepare_kernel(const AttnArgs p, int n_count, int ctas, uint8_t* ws) {
+  __shared__ uint8_t flags[kListTiles];
+  __shared__ uint16_t listed[kListElements];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.seq, n_kv = (S + BKV - 1) / BKV, n_qp = (S + 2 * BQ - 1) / (2 * BQ);
+  ListWorkspace w;
+  list_workspace(ws, p.batch, n_kv, ctas, &w);
+  for (int i = blockIdx.x * kPrepareThreads + threadIdx.x; i < n_count; i += gridDim.x * kPrepareThreads) p.count[i] = 0;
+  for (int i = warp; i < p.batch * n_kv; i += kPrepareThreads / 32) {
+    const uint8_t* km = p.key_mask + (size_t)(i / n_kv) * S;
+    bool any = false, off = false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int kc = i % n_kv * BKV + q * 32 + lane;
+      const bool on = kc < S && km[kc < S ? kc : 0] != 0;
+      any |= on;
+      off |= !on;
+    }
+    any = __any_sync(0xffffffffu, any) != 0;
+    off = __any_sync(0xffffffffu, off) != 0;
+    if (lane == 0) flags[i] = (uint8_t)((any ? 1 : 0) | (off ? 2 : 0));
+  }
+  __syncthreads();
+  for (int e = warp; e < p.batch; e += kPrepareThreads / 32) {
+    int n = 0;
+    for (int j0 = 0; j0 < n_kv; j0 += 32) {
+      const int j = j0 + lane;
+      const uint8_t f = j < n_kv ? flags[e * n_kv + j] : (uint8_t)0;
+      const uint32_t word = __ballot_sync(0xffffffffu, (f & 1) != 0);
+      if (blockIdx.x == 0 && (f & 1))
+        w.list[e * n_kv + n + __popc(word & ((1u << lane) - 1u))] = (uint16_t)(j | ((f & 2) ? kListPartial : 0));
+      n += __popc(word);
+    }
+    if (lane == 0) listed[e] = (uint16_t)n;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && (int)threadIdx.x < ctas)
+    w.seg_count[threadIdx.x] = build_masked_segments(w.seg + threadIdx.x * kMaxSegs, listed, n_kv, p.batch, p.n_heads * n_qp,
+                                                     (int)threadIdx.x, ctas);
+  for (int e = 0; e < p.batch; ++e) {
+    if (listed[e] > 0) continue;
+    const long long vecs = (long long)S * p.n_heads * (kHeadDim / 8), rows = (long long)S * p.n_heads;
+    uint4* o = reinterpret_cast<uint4*>(p.out) + e * vecs;
+    float* l = p.lse + e * rows;
+    const long long first = (long long)blockIdx.x * kPrepareThreads + threadIdx.x, stride = (long long)gridDim.x * kPrepareThreads;
+    for (long long i = first; i < vecs; i += stride) o[i] = make_uint4(0, 0, 0, 0);
+    for (long long i = first; i < rows; i += stride) l[i] = neg_inf();
+  }
+}
+
 // 12 warps, 3 per SM sub-partition (16K registers each): 168 registers per thread at launch, which
 // the launch bound below lets the compiler derive; the roles then trade registers as above.
 //
@@ -114,7 +242,9 @@ __device__ int build_segments(int4* tab, long long total, int n_kv) {
 // recomputes the probabilities, and it clears the V rows of masked keys in shared memory (the wait
 // proxy does, which has V of each key tile before the MMA issuer may use it): their probabilities are
 // zero, but zero times an infinity or NaN in a padded row would not be.
-template <bool kLse>
+//
+// kList: that forward with a mask on the split schedule, with the list and the segments above.
+template <bool kLse, bool kList>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const AttnArgs p) {
@@ -164,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    *seg_count = build_segments(seg_tab, (long long)p.batch * p.n_heads * n_qp * n_kv, n_kv);
+    if (!kList) *seg_count = build_segments(seg_tab, (long long)p.batch * p.n_heads * n_qp * n_kv, n_kv);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -177,6 +307,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   grid_dep_wait();  // q, k and v are the previous kernel's outputs
   grid_dep_launch();
+
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + OFF_LIST);
+  if (kList) {
+    ListWorkspace w;
+    list_workspace(p.list_ws, p.batch, n_kv, (int)gridDim.x, &w);
+    for (int i = threadIdx.x; i < p.batch * n_kv; i += kThreads) list[i] = w.list[i];
+    if (threadIdx.x < kMaxSegs) seg_tab[threadIdx.x] = w.seg[blockIdx.x * kMaxSegs + threadIdx.x];
+    if (threadIdx.x == 0) *seg_count = w.seg_count[blockIdx.x];
+    __syncthreads();
+  }
+  auto tile_at = [&](int place) { return kList ? (int)list[place] & (kListPartial - 1) : place; };
 
   // The two register regions are separate branches (warpgroup-uniform: every warp of a warpgroup
   // takes the same one), so the compiler holds each role to its own register budget.
@@ -206,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(sQ + TILE_BYTES, &tmQ, q_full, 0, q0 + BQ, bh);
           tma_load_3d(sQ + TILE_BYTES + HALF_BYTES, &tmQ, q_full, 64, q0 + BQ, bh);
           ++seg;
-          for (int j = sg.y; j < sg.z; ++j, ++kt) {
+          for (int place = sg.y; place < (kList ? sg.y + sg.z : sg.z); ++place, ++kt) {
+            const int j = tile_at(place);
             const int st = (kt & 1);
             const uint32_t ph = (uint32_t)((kt >> 1) & 1);
             if (!mbar_wait(&k_empty[st], ph ^ 1u, abort_flag, p.err, DEV_TIMEOUT_ATTN + 1)) {
@@ -246,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kt = 0;
       bool ok = true;
       for (int seg = 0; ok && seg < n_seg; ++seg) {
-        const int n = seg_tab[seg].z - seg_tab[seg].y;
+        const int n = kList ? seg_tab[seg].z : seg_tab[seg].z - seg_tab[seg].y;
         for (int t = 0; t < n; ++t, ++kt) {
           // each arrival belongs to the phase of key tile kt: the previous phase of the barrier
           // must be complete first (the copies often land a key tile ahead of the softmax)
@@ -254,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t bad[4] = {0, 0, 0, 0};
           if (kLse && p.key_mask != nullptr) {
             const int4 sg = seg_tab[seg];
-            masked_keys(p.key_mask + (size_t)(sg.x / n_qp / p.n_heads) * S, (sg.y + t) * BKV, S, lane, bad);
+            if (!kList || (list[sg.y + t] & kListPartial))
+              masked_keys(p.key_mask + (size_t)(sg.x / n_qp / p.n_heads) * S, tile_at(sg.y + t) * BKV, S, lane, bad);
           }
           if ((kt > 0 && !mbar_wait_warp(&p_full[0], prev, abort_flag, p.err, DEV_TIMEOUT_ATTN + 9)) ||
               !mbar_wait_warp(&v_full[kt & 1], (uint32_t)((kt >> 1) & 1), abort_flag, p.err, DEV_TIMEOUT_ATTN + 9)) {
@@ -317,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kt = 0;
       bool ok = true;
       for (int seg = 0; ok && seg < n_seg; ++seg) {
-        const int n = seg_tab[seg].z - seg_tab[seg].y;
+        const int n = kList ? seg_tab[seg].z : seg_tab[seg].z - seg_tab[seg].y;
         const int kt0 = kt;
         ok = mbar_wait_warp(q_full, (uint32_t)(seg & 1), abort_flag, p.err, DEV_TIMEOUT_ATTN + 3) &&
              mbar_wait_warp(&k_full[kt0 & 1], (uint32_t)((kt0 >> 1) & 1), abort_flag, p.err, DEV_TIMEOUT_ATTN + 3);
@@ -440,11 +583,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_run = neg_inf();  // reference max (base-2 units) the exponents are taken against
       float l_run = 0.0f;
       const int jb = seg_tab[seg].y;
-      const int n = seg_tab[seg].z - jb;
+      const int n = kList ? seg_tab[seg].z : seg_tab[seg].z - seg_tab[seg].y;
       const int kt0 = kt;
       for (int t = 0; t < n; ++t) {
         kt = kt0 + t;
-        const int j = jb + t;
+        const int entry = kList ? (int)list[jb + t] : 0;
+        const int j = kList ? entry & (kListPartial - 1) : jb + t;
         if (!mbar_wait_warp(&s_full[wg], (uint32_t)(kt & 1), abort_flag, p.err, DEV_TIMEOUT_ATTN + 8)) {
           ok = false;
           break;
@@ -456,7 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         const int kbase = j * BKV;
         uint32_t words[4];
-        if (smem_mask) {
+        if (kList && !(entry & kListPartial)) {
+          words[0] = words[1] = words[2] = words[3] = 0xffffffffu;
+        } else if (smem_mask) {
           const uint4 mw = *reinterpret_cast<const uint4*>(mask_words + j * 4);
           words[0] = mw.x;
           words[1] = mw.y;
@@ -559,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = bh % p.n_heads;
       const int row = (sg.x % n_qp) * (2 * BQ) + wg * BQ + r;
       __nv_bfloat16* dst_row = p.out + ((size_t)b * S + row) * H + (size_t)h * kHeadDim;
-      if (sg.y == 0 && sg.z == n_kv) {
+      if (kList ? sg.w == (kSegFirst | kSegLast) : (sg.y == 0 && sg.z == n_kv)) {
         // the whole unit: normalise and store
         const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
         if (kLse && row < S) p.lse[(size_t)bh * S + row] = row_lse(m_run, l_run);
@@ -586,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // slot (unnormalised O, laid out [32-column chunk][4-column group][row] so each warp store
         // covers 512 contiguous bytes, then m and l); the second of the two to arrive adds both,
         // in the fixed order first part + second part, and stores the normalised output.
-        const bool first_part = sg.y == 0;
+        const bool first_part = kList ? (sg.w & kSegFirst) != 0 : sg.y == 0;
         float* mine = p.part + (((size_t)blockIdx.x * 2 + (first_part ? 1 : 0)) * 2 + wg) * kPartTileFloats;
         float* other = p.part + ((((size_t)blockIdx.x + (first_part ? 1 : -1)) * 2 + (first_part ? 0 : 1)) * 2 + wg) *
                                     kPartTileFloats;
@@ -670,33 +816,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-template <bool kLse>
+template <bool kLse, bool kList>
 static cudaError_t attention_launch_as(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                        const AttnArgs& a, int num_sms, cudaStream_t s) {
+  constexpr int kSmem = kList ? SMEM_TOTAL_LIST : SMEM_TOTAL;
   static bool attr_done[kMaxDevices] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!attr_done[dev]) {
-    e = cudaFuncSetAttribute(attn_fwd_kernel<kLse>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+    e = cudaFuncSetAttribute(attn_fwd_kernel<kLse, kList>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     // the softmax warpgroups' register increase needs the pool the split was sized for
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, attn_fwd_kernel<kLse>);
+    e = cudaFuncGetAttributes(&fa, attn_fwd_kernel<kLse, kList>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs * kThreads < 128 * kRegsControl + 256 * kRegsSoftmax) return cudaErrorInvalidConfiguration;
     attr_done[dev] = true;
   }
-  return launch_kernel(attn_fwd_kernel<kLse>,
+  return launch_kernel(attn_fwd_kernel<kLse, kList>,
                        dim3(attention_grid(a.batch, a.seq, a.n_heads, a.part != nullptr ? num_sms : 0)),
-                       dim3(kThreads), SMEM_TOTAL, s, true, tq, tk, tv, a);
+                       dim3(kThreads), kSmem, s, true, tq, tk, tv, a);
 }
 
 cudaError_t attention_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const AttnArgs& a, int num_sms, cudaStream_t s) {
-  return a.lse != nullptr ? attention_launch_as<true>(tq, tk, tv, a, num_sms, s)
-                          : attention_launch_as<false>(tq, tk, tv, a, num_sms, s);
+  if (a.lse == nullptr) return attention_launch_as<false, false>(tq, tk, tv, a, num_sms, s);
+  return a.list_ws != nullptr ? attention_launch_as<true, true>(tq, tk, tv, a, num_sms, s)
+                              : attention_launch_as<true, false>(tq, tk, tv, a, num_sms, s);
 }
 
 // Units are split between CTAs (one per SM) only while there are at most 8 units per SM.  With
@@ -723,6 +871,23 @@ size_t attention_scratch_bytes(int batch, int seq, int n_heads, int num_sms) {
 size_t attention_count_bytes(int batch, int seq, int n_heads) {
   const long long units = (long long)batch * n_heads * ((seq + 2 * BQ - 1) / (2 * BQ));
   return ((size_t)units * 2 * sizeof(int) + 255) & ~(size_t)255;
+}
+
+// (Units to split are few, so the list fits: at most 8 per SM of 256 queries each.)
+size_t attention_list_bytes(int batch, int seq, int n_heads, int num_sms) {
+  const long long units = (long long)batch * n_heads * ((seq + 2 * BQ - 1) / (2 * BQ));
+  const int n_kv = (seq + BKV - 1) / BKV;
+  if (!attention_splits(units, num_sms) || num_sms > kPrepareThreads || batch > kListElements ||
+      (long long)batch * n_kv > kListTiles)
+    return 0;
+  ListWorkspace w;
+  return list_workspace(nullptr, batch, n_kv, num_sms, &w);
+}
+
+cudaError_t attention_prepare_launch(const AttnArgs& a, int num_sms, cudaStream_t s) {
+  const int n_count = (int)(attention_count_bytes(a.batch, a.seq, a.n_heads) / sizeof(int));
+  return launch_kernel(attn_prepare_kernel, dim3((unsigned)num_sms), dim3(kPrepareThreads), 0, s, true, a, n_count, num_sms,
+                       a.list_ws);
 }
 
 }  // namespace mi

@@ -69,6 +69,7 @@ struct AttnArgs {
   float* part;                 // partial results of split units, two slots per CTA
   int* count;                  // [units][2] arrival counters, zero at launch (left zero after it)
   float* lse;                  // [B, n_heads, S] log-sum-exp of each row's scaled scores, or null
+  uint8_t* list_ws;            // attention_list_bytes() bytes (16-byte aligned) or null: every key tile is walked
 };
 
 // q/k maps: 3-D over (128, S, B * n_heads); v map: 4-D over (128, n_heads, S, B) of the qkv buffer.
@@ -80,6 +81,10 @@ int attention_grid(int batch, int seq, int n_heads, int num_sms);
 // its arrival counters, which come first.
 size_t attention_scratch_bytes(int batch, int seq, int n_heads, int num_sms);
 size_t attention_count_bytes(int batch, int seq, int n_heads);
+// Workspace of the list of key tiles that the training forward walks with a mask (0 where it walks all), and
+// the kernel that fills it and clears the arrival counters.
+size_t attention_list_bytes(int batch, int seq, int n_heads, int num_sms);
+cudaError_t attention_prepare_launch(const AttnArgs& a, int num_sms, cudaStream_t s);
 
 // Gradient of the attention (attention_bwd.cu).
 struct AttnBwdArgs {

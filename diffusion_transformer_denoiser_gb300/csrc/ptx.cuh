@@ -217,21 +217,18 @@ __device__ __forceinline__ void masked_keys(const uint8_t* mask, int k0, int seq
 }
 
 // Clears those rows of a 128 x 128 bf16 tile (two 128-byte-swizzled halves of 16 KB: a row is 128
-// contiguous bytes of each half, whatever its swizzle), once the tile has landed; lanes 0-15 take one
-// row, lanes 16-31 the next.  Ordered before later MMAs of the tile.
+// contiguous bytes of each half, whatever its swizzle), once the tile has landed; lanes 0-15 take the
+// even rows, lanes 16-31 the odd ones.  Ordered before later MMAs of the tile.
 __device__ __forceinline__ void zero_rows(uint8_t* tile, const uint32_t (&bad)[4], int lane) {
   if ((bad[0] | bad[1] | bad[2] | bad[3]) == 0) return;
-  uint8_t* at = tile + ((lane >> 3) & 1) * 16384 + (lane & 7) * 16;
+  uint8_t* at = tile + ((lane >> 3) & 1) * 16384 + (lane & 7) * 16 + (lane >> 4) * 128;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    uint32_t m = bad[w];
-    while (m != 0) {
-      const int first = __ffs(m) - 1;
-      m &= m - 1;
-      const int second = m != 0 ? __ffs(m) - 1 : first;
-      m &= m - 1;
-      *reinterpret_cast<uint4*>(at + (w * 32 + (lane < 16 ? first : second)) * 128) = make_uint4(0, 0, 0, 0);
-    }
+    uint32_t m = bad[w] >> (lane >> 4);
+    if (bad[w] == 0) continue;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i, m >>= 2)
+      if (m & 1u) *reinterpret_cast<uint4*>(at + (w * 32 + 2 * i) * 128) = make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
 }

@@ -15,7 +15,7 @@ HEAD = 128
 
 def heads_of(t, batch, seq, heads):
     """[batch * seq, heads * 128] -> float64 [batch, heads, seq, 128]"""
-    return t.view(batch, seq, heads, HEAD).permute(0, 2, 1, 3).double()
+    return t.reshape(batch, seq, heads, HEAD).permute(0, 2, 1, 3).double()
 
 
 def attention64(q, k, v, mask, d_o=None, with_bounds=True):

@@ -135,6 +135,35 @@ def test_split_forward_with_many_units():
         c.check(mi, grads=False)
 
 
+@pytest.mark.parametrize("batch,heads,seq,valid", [
+    (2, 36, 4096, [(0, 4096), (4000, 4001)]),   # one element of 32 key tiles, one of a single tile
+    (1050, 1, 130, None),                       # more elements than are listed in shared memory
+    (600, 1, 130, None),
+    (5, 33, 513, [(0, 0), (0, 513), (512, 513), (0, 0), (128, 256)]),  # empty ones between, a last tile of one key
+    (2, 3, 1500, [(300, 301), (1499, 1500)])])  # one CTA per unit, the only tile in the middle or last
+def test_split_forward_with_uneven_padding(batch, heads, seq, valid):
+    """Elements with very different numbers of key tiles: every way the work is dealt out."""
+    mi = require_gpu()
+    c = Case(batch, heads, seq, None)
+    c.mask = torch.zeros(batch, seq, dtype=torch.uint8, device="cuda")
+    for b in range(batch):
+        lo, hi = valid[b] if valid else ((b * 7) % seq, seq) if b % 3 else (0, 0)
+        c.mask[b, lo:hi] = 1
+    if c.q.numel() * seq > 1 << 34:  # the 64-bit check takes some heads of the large case
+        c.forward(mi)
+        torch.cuda.synchronize()
+        assert mi.device_error() == 0
+        for h in (0, heads - 1):
+            cols = slice(h * HEAD, (h + 1) * HEAD)
+            r = attention64(c.q[:, h:h + 1].double(), c.k[:, h:h + 1].double(), heads_of(c.v[:, cols], batch, seq, 1), c.mask)
+            within(c.lse[:, h:h + 1], r["lse"], r["lse_tol"], "lse")
+            within(heads_of(c.o[:, cols], batch, seq, 1), r["o"], r["o_tol"], "o")
+        return
+    c.forward(mi)
+    c.backward(mi)
+    c.check(mi)
+
+
 @pytest.mark.parametrize("split", [False, True])
 def test_forward_equals_the_inference_call(split):
     mi = require_gpu()
