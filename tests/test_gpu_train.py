@@ -255,6 +255,24 @@ def test_outputs_end_where_they_should():
         assert (buf[used:] == 9.0).all()
 
 
+def test_outputs_aligned_to_16_bytes_only():
+    """Tensors that start 16 bytes behind a larger boundary give the bytes of those that do not."""
+    mi = require_gpu()
+    c, d = Case(1, 3, 333, "pad"), Case(1, 3, 333, "pad")
+    for name in ("q", "k", "qkv", "d_o", "o", "lse", "dq", "dk", "dqkv"):
+        t = getattr(d, name)
+        step = 16 // t.element_size()
+        buf = torch.empty(t.numel() + step, dtype=t.dtype, device="cuda")
+        view = buf[step:].view(t.shape)
+        assert view.data_ptr() % 32 == 16
+        setattr(d, name, view.copy_(t))
+    for x in (c, d):
+        x.forward(mi)
+        x.backward(mi)
+    d.check(mi)
+    assert all(torch.equal(x, y) for x, y in zip(c.bits(), d.bits()))
+
+
 def test_captured_and_replayed():
     """One graph of forward and gradient, replayed on other inputs, gives the bytes of plain calls."""
     mi = require_gpu()
