@@ -34,6 +34,11 @@
 //     rows (queries pass): zero times an infinity or NaN in a padded row would not be zero.
 //   * warps 4-11: two warpgroups, each half of the 128 streamed rows; one thread per lane.  They also read
 //     the accumulators out (queries pass: through shared memory, stored by TMA, a warp its own 32 rows).
+// Both passes are bound by the latency from a tile's scores to its P or dS, and sensitive to the length of
+// the code between: unit ends that are read and stored in rolled loops instead of straight code, and masks
+// that are applied in one place to the packed words, brought the 16418-row gradient from 6.9 to 6.05 ms (in
+// bursts; 6.7 ms at the power cap).  Four warpgroups with a quarter of the columns each, and MMAs issued from
+// loops, were slower (6.8 and 6.7 ms in bursts).
 // P and dS are rounded to bf16 once, as matrix operands; scores, D, sums and P in dS are fp32.
 #include "mi_internal.h"
 #include "ptx.cuh"
@@ -273,7 +278,7 @@ __device__ __forceinline__ void sum_ts(uint32_t d, uint32_t a, uint32_t half_col
 // 64 accumulator columns of a warp's 32 rows, scaled, as bf16 into its 4 KB of the staging tile
 // (128-byte rows, 16-byte pieces swizzled by the row as the TMA expects).
 __device__ __forceinline__ void stage64(uint8_t* out, uint32_t src, float f, int lane) {
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     uint32_t x[32];
     tmem_ld32(src + c * 32, x);
@@ -510,61 +515,49 @@ __device__ __forceinline__ void keys_proxy(const Pass& c) {
   }
 }
 
-// Warpgroup 0 stores dV, warpgroup 1 dK: first the row's accumulators as bf16 into registers (after which
-// they may be overwritten), then to memory.
-__device__ __forceinline__ void keys_read(uint32_t src, float f, uint32_t (&w)[64]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t x[32];
-    tmem_ld32(src + j * 32, x);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      w[16 * j + i] = pack_bf16x2(__uint_as_float(x[2 * i]) * f, __uint_as_float(x[2 * i + 1]) * f);
+// `wide`: dst is aligned to 32 bytes, else to 16.
+__device__ __forceinline__ void store_32_bytes(void* dst, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
-__device__ __forceinline__ void store_32_bytes(void* dst, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
-__device__ __forceinline__ void keys_store(const Pass& c, int id, int half, const uint32_t (&w)[64]) {
+// Warpgroup 0 stores dV, warpgroup 1 dK, 32 columns at a time.  A lane's row is a line of its own, and a store
+// costs a request per line: 16 bytes per lane took 7300 cycles of a unit, 32 bytes 3750.  So two lanes
+// exchange their pieces first and store 64 bytes of one row, then of the other (2600 cycles).
+__device__ __forceinline__ void keys_store(const Pass& c, int id, int half, uint32_t src, float f) {
   const AttnBwdArgs& p = *c.p;
   const int row = (id % c.n_tiles) * BT + (c.warp & 3) * 32 + c.lane, bh = id / c.n_tiles;
   const size_t stride = half == 0 ? (size_t)3 * p.n_heads * kHeadDim : kHeadDim;
   __nv_bfloat16* base = half == 0 ? p.dv + (size_t)(bh / p.n_heads) * p.seq * stride + (size_t)(bh % p.n_heads) * kHeadDim
                                   : p.dkp + (size_t)bh * p.seq * kHeadDim;
-  // A lane's row is a line of its own, and a store costs a request per line: 16 bytes per lane took 7300 cycles
-  // of a unit, 32 bytes 3750.  So two lanes exchange their pieces first and store 64 bytes of one row, then
-  // of the other.  An output that is only 16-byte aligned goes 16 bytes at a time.
-  if ((reinterpret_cast<uintptr_t>(base) & 31) == 0) {
-    const bool odd = c.lane & 1;
-    const int even_row = row & ~1;
-    __nv_bfloat16* even = base + (size_t)even_row * stride + (odd ? 16 : 0);
+  const bool odd = c.lane & 1, wide = (reinterpret_cast<uintptr_t>(base) & 31) == 0;
+  const int even_row = row & ~1;
+  __nv_bfloat16* even = base + (size_t)even_row * stride + (odd ? 16 : 0);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x[32], a[8], b[8];
+    tmem_ld32(src + i * 32, x);
+    tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t a[8], b[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t lo = w[16 * i + e], hi = w[16 * i + 8 + e];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
-        a[e] = odd ? got : lo;
-        b[e] = odd ? hi : got;
-      }
-      if (even_row < p.seq) store_32_bytes(even + 32 * i, a);
-      if (even_row + 1 < p.seq) store_32_bytes(even + stride + 32 * i, b);
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t lo = pack_bf16x2(__uint_as_float(x[2 * e]) * f, __uint_as_float(x[2 * e + 1]) * f);
+      const uint32_t hi = pack_bf16x2(__uint_as_float(x[16 + 2 * e]) * f, __uint_as_float(x[16 + 2 * e + 1]) * f);
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+      a[e] = odd ? got : lo;
+      b[e] = odd ? hi : got;
     }
-  } else if (row < p.seq) {
-    uint4* dst = reinterpret_cast<uint4*>(base + (size_t)row * stride);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    if (even_row < p.seq) store_32_bytes(even + 32 * i, a, wide);
+    if (even_row + 1 < p.seq) store_32_bytes(even + stride + 32 * i, b, wide);
   }
 }
 
-// The CTA's last keys unit is stored behind the barrier between the passes (its accumulators are in registers
-// by then), while the first tiles of the queries pass land.
+// Ends at the barrier between the passes.
 __device__ __forceinline__ void keys_compute(const Pass& c) {
   const AttnBwdArgs& p = *c.p;
   Bars* bars = c.bars;
@@ -585,9 +578,10 @@ __device__ __forceinline__ void keys_compute(const Pass& c) {
       break;
     }
     const int row = (id % c.n_tiles) * BT + r;
-    bool row_ok = row < p.seq;
-    if (row_ok && p.key_mask != nullptr) row_ok = p.key_mask[(size_t)(id / c.n_tiles / p.n_heads) * p.seq + row] != 0;
-    const bool rows_ok = __all_sync(0xffffffffu, row_ok) != 0;
+    // (read here, looked at when the first scores are there)
+    uint32_t row_mask = row < p.seq;
+    if (row < p.seq && p.key_mask != nullptr) row_mask = p.key_mask[(size_t)(id / c.n_tiles / p.n_heads) * p.seq + row];
+    bool row_ok = true, rows_ok = true;
     for (int n = 0; n < c.n_tiles; ++n, ++g) {
       const uint32_t st = g & 1u, ph = g & 1u;
       // the statistics land with dO, well before the scores are there
@@ -607,6 +601,10 @@ __device__ __forceinline__ void keys_compute(const Pass& c) {
       uint32_t pr[64], pk[32];
       tmem_ld32(t_s, pr);
       tmem_ld32(t_s + 32, pr + 32);
+      if (n == 0) {
+        row_ok = row_mask != 0;
+        rows_ok = __all_sync(0xffffffffu, row_ok) != 0;
+      }
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -616,12 +614,12 @@ __device__ __forceinline__ void keys_compute(const Pass& c) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) pr[4 * i + e] = __float_as_uint(ex2_approx(z[e]));
       }
-      if (!rows_ok) {  // a masked key's scores may be anything
-#pragma unroll
-        for (int i = 0; i < 64; ++i) pr[i] = row_ok ? pr[i] : 0u;
-      }
 #pragma unroll
       for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(__uint_as_float(pr[2 * i]), __uint_as_float(pr[2 * i + 1]));
+      if (!rows_ok) {  // a masked key's scores may be anything
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pk[i] = row_ok ? pk[i] : 0u;
+      }
       tmem_st32(t_s, pk);
       tmem_st_wait();
       if (n == 0 && before >= 0) {
@@ -630,17 +628,11 @@ __device__ __forceinline__ void keys_compute(const Pass& c) {
           break;
         }
         tc_fence_after();
-        uint32_t w[64];
-        keys_read(t_acc, f_acc, w);
-        tc_fence_before();
-        __syncwarp();
-        if (c.lane == 0) mbar_arrive(&bars->p_full);
-        keys_store(c, before, half, w);
-      } else {
-        tc_fence_before();
-        __syncwarp();
-        if (c.lane == 0) mbar_arrive(&bars->p_full);
+        keys_store(c, before, half, t_acc, f_acc);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive(&bars->p_full);
       float4 nd[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) nd[i] = stat[32 + i];
@@ -664,13 +656,13 @@ __device__ __forceinline__ void keys_compute(const Pass& c) {
           f2_unpack(f2_mul(f2_add(pair_of(dp + 4 * i), f2_pack(nd[i].x, nd[i].y)), pair_of(pr + 32 * j + 4 * i)), z[0], z[1]);
           f2_unpack(f2_mul(f2_add(pair_of(dp + 4 * i + 2), f2_pack(nd[i].z, nd[i].w)), pair_of(pr + 32 * j + 4 * i + 2)), z[2],
                     z[3]);
-          if (!rows_ok) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = row_ok ? z[e] : 0.0f;
-          }
           pk[16 * j + 2 * i] = pack_bf16x2(z[0], z[1]);
           pk[16 * j + 2 * i + 1] = pack_bf16x2(z[2], z[3]);
         }
+      }
+      if (!rows_ok) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pk[i] = row_ok ? pk[i] : 0u;
       }
       tmem_st32(t_dp, pk);
       tmem_st_wait();
@@ -684,14 +676,12 @@ __device__ __forceinline__ void keys_compute(const Pass& c) {
     const int next_id = c.unit(k + 1);
     if (next_id < 0) {
       const bool done = next_id == -1 && c.wait(&bars->acc_done, (uint32_t)(k & 1), 13);
-      uint32_t w[64];
       if (done) {
         tc_fence_after();
-        keys_read(t_acc, f_acc, w);
+        keys_store(c, id, half, t_acc, f_acc);
       }
       tc_fence_before();
       __syncthreads();
-      if (done) keys_store(c, id, half, w);
       return;
     }
   }
@@ -868,10 +858,29 @@ __device__ __forceinline__ void queries_proxy(const Pass& c) {
     const int b = id / c.n_tiles / p.n_heads;
     const int count = c.walked(b);
     const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + (size_t)b * p.seq : nullptr;
+    // with a mask: which of this lane's keys of the next tile are masked, read a tile ahead
+    bool off[4] = {false, false, false, false};
+    auto read_mask = [&](int t) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int kc = t * BT + w * 32 + c.lane;
+        off[w] = kc < p.seq && mask[kc < p.seq ? kc : 0] == 0;
+      }
+    };
+    int t_ahead = 0;
+    if (mask != nullptr) {
+      read_mask(c.tile(b, 0));
+      if (count > 1) t_ahead = c.tile(b, 1);
+    }
     for (int n = 0; n < count; ++n, ++g, x.next(), y.next()) {
       // K of tile g, clean: an arrival of phase g - 1 of s_read (phase g - 2 complete)
       uint32_t bad[4] = {0, 0, 0, 0};
-      if (mask != nullptr) masked_keys(mask, c.tile(b, n) * BT, p.seq, c.lane, bad);
+      if (mask != nullptr) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) bad[w] = __ballot_sync(0xffffffffu, off[w]);
+        if (n + 1 < count) read_mask(t_ahead);
+        if (n + 2 < count) t_ahead = c.tile(b, n + 2);
+      }
       if ((g > 1 && !c.wait(&bars->s_read, g & 1u, 7)) || !c.wait(&bars->x_full[x.st], x.ph, 7)) {
         ok = false;
         break;
@@ -965,6 +974,7 @@ __device__ __forceinline__ void queries_compute(const Pass& c, const CUtensorMap
       }
     };
     read_mask(c.tile(b, 0));
+    int t_ahead = count > 1 ? c.tile(b, 1) : 0;
     for (int n = 0; n < count; ++n, ++g) {
       const uint32_t ph = g & 1u;
       const bool turn = n + 1 == count;  // the next tile is a new unit's
@@ -974,7 +984,8 @@ __device__ __forceinline__ void queries_compute(const Pass& c, const CUtensorMap
         if (next_id >= 0) read_row(next_id);
         ok = next_id != -2;
       } else {
-        read_mask(c.tile(b, n + 1));
+        read_mask(t_ahead);
+        if (n + 2 < count) t_ahead = c.tile(b, n + 2);
       }
       if (!ok || !c.wait(&bars->s_full, ph, 10)) {
         ok = false;

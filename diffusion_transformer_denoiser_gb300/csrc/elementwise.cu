@@ -550,34 +550,45 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const float* __restrict_
     if (r + stride < rows) read(r + stride);
     float c[4], s[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p = at[i];
-      const float t = p * hi[i];
-      float rest = fmaf(p, lo[i], fmaf(p, hi[i], -t));
-      rest -= rintf(rest);
-      const float frac = t - rintf(t);
+    for (int i = 0; i < 4; i += 2) {  // two pairs at a time in packed arithmetic
+      const f32x2_t p = f2_pack(at[i], at[i + 1]), h = f2_pack(hi[i], hi[i + 1]), l = f2_pack(lo[i], lo[i + 1]);
+      const f32x2_t t = f2_mul(p, h);
+      const f32x2_t left = f2_fma(p, l, f2_fma(p, h, f2_mul(t, f2_of(-1.0f))));
+      float t0, t1, l0, l1;
+      f2_unpack(t, t0, t1);
+      f2_unpack(left, l0, l1);
+      const f32x2_t frac = f2_add(t, f2_pack(-rintf(t0), -rintf(t1)));
+      const f32x2_t rest = f2_add(left, f2_pack(-rintf(l0), -rintf(l1)));
       constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number in the low bits
-      const float nb = fmaf(frac + rest, 4.0f, kMagic);
-      const uint32_t quarter = __float_as_uint(nb);
-      const float x = (fmaf(nb - kMagic, -0.25f, frac) + rest) * 6.283185307179586f;
-      const float x2 = x * x;
-      float sp = fmaf(x2, 2.75573192e-6f, -1.98412698e-4f);   // 1/9!, -1/7!
-      sp = fmaf(x2, sp, 8.33333333e-3f);                      // 1/5!
-      sp = fmaf(x2, sp, -1.66666667e-1f);                     // -1/3!
-      const float sv = fmaf(x * x2, sp, x);
-      float cp = fmaf(x2, -2.75573192e-7f, 2.48015873e-5f);   // -1/10!, 1/8!
-      cp = fmaf(x2, cp, -1.38888889e-3f);                     // -1/6!
-      cp = fmaf(x2, cp, 4.16666667e-2f);                      // 1/4!
-      cp = fmaf(x2, cp, -0.5f);
-      const float cv = fmaf(x2, cp, 1.0f);
-      // a quarter turn on: (c, s) -> (-s, c)
-      const bool odd = quarter & 1u;
-      const uint32_t cq = __float_as_uint(odd ? sv : cv), sq = __float_as_uint(odd ? cv : sv);
-      c[i] = __uint_as_float(cq ^ (((quarter + 1u) & 2u) << 30));
-      s[i] = __uint_as_float(sq ^ ((quarter & 2u) << 30));
+      const f32x2_t nb = f2_fma(f2_add(frac, rest), f2_of(4.0f), f2_of(kMagic));
+      const f32x2_t turn = f2_add(f2_fma(f2_add(nb, f2_of(-kMagic)), f2_of(-0.25f), frac), rest);
+      const f32x2_t x = f2_mul(turn, f2_of(6.283185307179586f));
+      const f32x2_t x2 = f2_mul(x, x);
+      f32x2_t sp = f2_fma(x2, f2_of(2.75573192e-6f), f2_of(-1.98412698e-4f));  // 1/9!, -1/7!
+      sp = f2_fma(x2, sp, f2_of(8.33333333e-3f));                               // 1/5!
+      sp = f2_fma(x2, sp, f2_of(-1.66666667e-1f));                              // -1/3!
+      sp = f2_fma(f2_mul(x, x2), sp, x);
+      f32x2_t cp = f2_fma(x2, f2_of(-2.75573192e-7f), f2_of(2.48015873e-5f));   // -1/10!, 1/8!
+      cp = f2_fma(x2, cp, f2_of(-1.38888889e-3f));                              // -1/6!
+      cp = f2_fma(x2, cp, f2_of(4.16666667e-2f));                               // 1/4!
+      cp = f2_fma(x2, cp, f2_of(-0.5f));
+      cp = f2_fma(x2, cp, f2_of(1.0f));
+      float sv[2], cv[2], nv[2];
+      f2_unpack(sp, sv[0], sv[1]);
+      f2_unpack(cp, cv[0], cv[1]);
+      f2_unpack(nb, nv[0], nv[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // a quarter turn on: (c, s) -> (-s, c)
+        const uint32_t quarter = __float_as_uint(nv[e]);
+        const bool odd = quarter & 1u;
+        const uint32_t cq = __float_as_uint(odd ? sv[e] : cv[e]), sq = __float_as_uint(odd ? cv[e] : sv[e]);
+        c[i + e] = __uint_as_float(cq ^ (((quarter + 1u) & 2u) << 30));
+        s[i + e] = __uint_as_float(sq ^ ((quarter & 2u) << 30));
+      }
     }
-    *reinterpret_cast<float4*>(cosv + r * 64 + j0) = make_float4(c[0], c[1], c[2], c[3]);
-    *reinterpret_cast<float4*>(sinv + r * 64 + j0) = make_float4(s[0], s[1], s[2], s[3]);
+    // evict-first: a table larger than the L2 cache does not push out what the consumers read next
+    __stcs(reinterpret_cast<float4*>(cosv + r * 64 + j0), make_float4(c[0], c[1], c[2], c[3]));
+    __stcs(reinterpret_cast<float4*>(sinv + r * 64 + j0), make_float4(s[0], s[1], s[2], s[3]));
   }
 }
 

@@ -476,6 +476,8 @@ __device__ __forceinline__ f32x2_t f2_pack(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ f32x2_t f2_of(float both) { return f2_pack(both, both); }
+
 __device__ __forceinline__ void f2_unpack(f32x2_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
