@@ -155,11 +155,28 @@ def _ptr(t: Optional[torch.Tensor], dtype=None) -> Optional[int]:
     return t.data_ptr()
 
 
-def _sized(t: torch.Tensor, dtype, n: int, name: str) -> int:
-    """_ptr of a tensor of n elements: the library sees pointers only, so a wrong size is refused here."""
+def _sized(t: torch.Tensor, dtype, n: int, name: str, device: int) -> int:
+    """_ptr of a tensor of n elements on GPU `device`: the library sees pointers only, so a wrong size or place is
+    refused here."""
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
-    return _ptr(t, dtype)
+    if t.get_device() != device:
+        raise ValueError(f"{name} must live on the GPU of the other tensors, cuda:{device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _on_current(t: torch.Tensor, name: str) -> int:
+    """The GPU of the call's first tensor, which has to be the current one (its stream and its kernels run there)."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must live on the GPU")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{name} lives on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    return device
 
 
 _BF = torch.bfloat16
@@ -330,9 +347,10 @@ def rope_axes_tables(positions, axis_pairs, rope_cos, rope_sin, theta=10000.0, s
     if positions.dim() != 2 or positions.shape[1] != len(axis_pairs):
         raise ValueError(f"positions {tuple(positions.shape)} must be [rows, {len(axis_pairs)}], one column per axis")
     rows, n = positions.shape
-    _check(lib().mi_rope_axes_tables(_ptr(positions, torch.float32), rows, n, (_I * n)(*axis_pairs), theta,
-                                     _sized(rope_cos, torch.float32, rows * 64, "rope_cos"),
-                                     _sized(rope_sin, torch.float32, rows * 64, "rope_sin"), _stream(stream)))
+    d, f32 = _on_current(positions, "positions"), torch.float32
+    _check(lib().mi_rope_axes_tables(_sized(positions, f32, rows * n, "positions", d), rows, n, (_I * n)(*axis_pairs), theta,
+                                     _sized(rope_cos, f32, rows * 64, "rope_cos", d),
+                                     _sized(rope_sin, f32, rows * 64, "rope_sin", d), _stream(stream)))
 
 
 def time_advance(t, dt, stream=None):
@@ -402,12 +420,13 @@ def attention(qp, kp, qkv, key_mask, o, batch, seq, n_heads, stream=None, ws=Non
 def attention_lse(qp, kp, qkv, key_mask, o, lse, batch, seq, n_heads, ws=None, stream=None):
     """attention that also stores lse [batch, heads, seq] (fp32) for attention_backward; `ws` as for attention."""
     rows = batch * n_heads * seq
-    n = rows * 128
+    n, d = rows * 128, _on_current(qp, "qp")
     ws_bytes = 0 if ws is None else ws.numel()
-    _check(lib().mi_attention_lse(_sized(qp, _BF, n, "qp"), _sized(kp, _BF, n, "kp"), _sized(qkv, _BF, 3 * n, "qkv"),
-                                  None if key_mask is None else _sized(key_mask, torch.uint8, batch * seq, "key_mask"),
-                                  _sized(o, _BF, n, "o"), _sized(lse, torch.float32, rows, "lse"), batch, seq, n_heads,
-                                  _ptr(ws, torch.uint8) if ws_bytes else None, ws_bytes, _stream(stream)))
+    _check(lib().mi_attention_lse(
+        _sized(qp, _BF, n, "qp", d), _sized(kp, _BF, n, "kp", d), _sized(qkv, _BF, 3 * n, "qkv", d),
+        None if key_mask is None else _sized(key_mask, torch.uint8, batch * seq, "key_mask", d), _sized(o, _BF, n, "o", d),
+        _sized(lse, torch.float32, rows, "lse", d), batch, seq, n_heads,
+        _sized(ws, torch.uint8, ws_bytes, "ws", d) if ws_bytes else None, ws_bytes, _stream(stream)))
 
 
 def attention_backward_workspace_size(batch, seq, n_heads) -> int:
@@ -419,13 +438,13 @@ def attention_backward_workspace_size(batch, seq, n_heads) -> int:
 def attention_backward(qp, kp, qkv, key_mask, o, lse, d_o, dqp, dkp, dqkv, batch, seq, n_heads, ws, stream=None):
     """Gradients of attention_lse: dqp, dkp, and dv in the v columns of dqkv (its q and k columns are left alone)."""
     rows = batch * n_heads * seq
-    n = rows * 128
+    n, d = rows * 128, _on_current(qp, "qp")
     _check(lib().mi_attention_backward(
-        _sized(qp, _BF, n, "qp"), _sized(kp, _BF, n, "kp"), _sized(qkv, _BF, 3 * n, "qkv"),
-        None if key_mask is None else _sized(key_mask, torch.uint8, batch * seq, "key_mask"), _sized(o, _BF, n, "o"),
-        _sized(lse, torch.float32, rows, "lse"), _sized(d_o, _BF, n, "d_o"), _sized(dqp, _BF, n, "dqp"),
-        _sized(dkp, _BF, n, "dkp"), _sized(dqkv, _BF, 3 * n, "dqkv"), batch, seq, n_heads, _ptr(ws, torch.uint8),
-        ws.numel(), _stream(stream)))
+        _sized(qp, _BF, n, "qp", d), _sized(kp, _BF, n, "kp", d), _sized(qkv, _BF, 3 * n, "qkv", d),
+        None if key_mask is None else _sized(key_mask, torch.uint8, batch * seq, "key_mask", d), _sized(o, _BF, n, "o", d),
+        _sized(lse, torch.float32, rows, "lse", d), _sized(d_o, _BF, n, "d_o", d), _sized(dqp, _BF, n, "dqp", d),
+        _sized(dkp, _BF, n, "dkp", d), _sized(dqkv, _BF, 3 * n, "dqkv", d), batch, seq, n_heads,
+        _sized(ws, torch.uint8, ws.numel(), "ws", d), ws.numel(), _stream(stream)))
 
 
 def qk_norm_rope_backward_workspace_size(batch, seq, n_heads) -> int:
@@ -442,13 +461,14 @@ def qk_norm_rope_backward(qkv, q_norm_w, k_norm_w, rope_cos, rope_sin, dqp, dkp,
     if rope_cos.numel() < table or rope_sin.numel() < table:
         raise ValueError(f"rope_cos, rope_sin have {rope_cos.numel()}, {rope_sin.numel()} elements, too few for {batch} "
                          f"tables of {seq} rows, {rope_bstride} apart")
-    f32 = torch.float32
+    d, f32 = _on_current(qkv, "qkv"), torch.float32
     _check(lib().mi_qk_norm_rope_backward(
-        _sized(qkv, _BF, 3 * n, "qkv"), _sized(q_norm_w, _BF, 128, "q_norm_w"), _sized(k_norm_w, _BF, 128, "k_norm_w"),
-        _ptr(rope_cos, f32), _ptr(rope_sin, f32), rope_bstride, _sized(dqp, _BF, n, "dqp"), _sized(dkp, _BF, n, "dkp"),
-        _sized(dqkv, _BF, 3 * n, "dqkv"), _sized(dq_norm_w, f32, 128, "dq_norm_w"),
-        _sized(dk_norm_w, f32, 128, "dk_norm_w"), batch, seq, n_heads, eps, _ptr(ws, torch.uint8), ws.numel(),
-        _stream(stream)))
+        _sized(qkv, _BF, 3 * n, "qkv", d), _sized(q_norm_w, _BF, 128, "q_norm_w", d),
+        _sized(k_norm_w, _BF, 128, "k_norm_w", d), _sized(rope_cos, f32, rope_cos.numel(), "rope_cos", d),
+        _sized(rope_sin, f32, rope_sin.numel(), "rope_sin", d), rope_bstride, _sized(dqp, _BF, n, "dqp", d),
+        _sized(dkp, _BF, n, "dkp", d), _sized(dqkv, _BF, 3 * n, "dqkv", d), _sized(dq_norm_w, f32, 128, "dq_norm_w", d),
+        _sized(dk_norm_w, f32, 128, "dk_norm_w", d), batch, seq, n_heads, eps,
+        _sized(ws, torch.uint8, ws.numel(), "ws", d), ws.numel(), _stream(stream)))
 
 
 def gated_add(x, y, mod, gate_row, out, batch, seq, stream=None):

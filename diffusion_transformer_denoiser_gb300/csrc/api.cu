@@ -906,8 +906,10 @@ static mi_status check_train_shape(int batch, int seq, int n_heads) {
   if (batch <= 0 || seq <= 0 || n_heads <= 0) return fail(MI_ERR_INVALID_ARG, "batch, seq, n_heads must be positive");
   if (seq > (1 << 20)) return fail(MI_ERR_UNSUPPORTED, "seq=%d: at most 2^20 rows", seq);
   if (n_heads > 1024) return fail(MI_ERR_UNSUPPORTED, "n_heads=%d: at most 1024", n_heads);
-  if ((long long)batch * seq * n_heads > (1LL << 30))
-    return fail(MI_ERR_UNSUPPORTED, "batch * seq * n_heads = %lld: at most 2^30", (long long)batch * seq * n_heads);
+  const long long tiles = (seq + 127) / 128;
+  if (batch > (1LL << 23) / (tiles * n_heads))
+    return fail(MI_ERR_UNSUPPORTED, "batch * n_heads * (seq in tiles of 128 rows) = %lld: at most 2^23",
+                (long long)batch * n_heads * tiles);
   return MI_OK;
 }
 
@@ -1244,8 +1246,11 @@ mi_status mi_rope_axes_tables(const float* positions, int rows, int n_axes, cons
   for (int a = 0; a < n_axes; ++a) {
     if (axis_pairs[a] <= 0 || axis_pairs[a] > 64 - at)
       return fail(MI_ERR_INVALID_ARG, "axis_pairs must be positive and add up to 64 (axis %d: %d)", a, axis_pairs[a]);
-    for (int j = 0; j < axis_pairs[a]; ++j, ++at) {
-      const double turns = pow((double)theta, -(double)j / axis_pairs[a]) / 6.283185307179586476925;
+    // (a running product: 64 calls of pow would take longer than the launch; j roundings of 2^-53 on a frequency
+    // that falls as theta^(-j / pairs) stay below the 2^-48 that hi + lo keep)
+    const double step = pow((double)theta, -1.0 / axis_pairs[a]);
+    double turns = 1.0 / 6.283185307179586476925;
+    for (int j = 0; j < axis_pairs[a]; ++j, ++at, turns *= step) {
       f.hi[at] = (float)turns;
       f.lo[at] = (float)(turns - (double)f.hi[at]);
       f.axis[at] = (unsigned char)a;

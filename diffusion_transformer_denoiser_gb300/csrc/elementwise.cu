@@ -703,8 +703,7 @@ cudaError_t qk_norm_rope_bwd_launch(const __nv_bfloat16* qkv, const __nv_bfloat1
   if (qk_bwd_one_cluster(qk_bwd_items(batch, seq, n_heads)))
     return launch_kernel_cluster(qk_norm_rope_bwd_kernel<true>, dim3(grid), dim3(kQkBwdThreads), kQkCluster, s, qkv, wq, wk,
                                  cos, sin, rope_bstride, dqp, dkp, dqkv, partial, dwq, dwk, batch, seq, n_heads, eps);
-  cudaError_t e = launch_kernel(qk_norm_rope_bwd_kernel<false>, dim3(grid), dim3(kQkBwdThreads), 0, s,
-                                launch_early(grid, num_sms), qkv, wq, wk,
+  cudaError_t e = launch_kernel(qk_norm_rope_bwd_kernel<false>, dim3(grid), dim3(kQkBwdThreads), 0, s, true, qkv, wq, wk,
                                 cos, sin, rope_bstride, dqp, dkp, dqkv, partial, dwq, dwk, batch, seq, n_heads, eps);
   if (e != cudaSuccess) return e;
   return launch_kernel(qk_gain_sum_kernel, dim3(16), dim3(256), 0, s, true, (const float*)partial, grid, dwq, dwk);
@@ -763,8 +762,7 @@ cudaError_t rope_axes_launch(const float* pos, int rows, int n_axes, const RopeA
   const int need = (rows + 15) / 16;
   const int cap = 4 * num_sms;
   const int grid = need < cap ? need : cap;
-  return launch_kernel(rope_axes_kernel, dim3(grid), dim3(256), 0, s, launch_early(grid, num_sms), pos, rows, n_axes, f, cosv,
-                       sinv);
+  return launch_kernel(rope_axes_kernel, dim3(grid), dim3(256), 0, s, true, pos, rows, n_axes, f, cosv, sinv);
 }
 
 cudaError_t timestep_embedding_launch(const float* t, __nv_bfloat16* out, int batch, int dim, double scale,

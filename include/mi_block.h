@@ -66,7 +66,8 @@ mi_status mi_device_error(int* code);
 /* Error codes mi_device_error reports: 0x100 + k (a GEMM wait), 0x200 + k (an attention wait),
  * 0x300 (the self-test below), 0x400 (a GEMM whose split of tail tiles over the CTAs has more parts
  * per tile than its fix-up adds; the library's own plans never produce one), 0x500 + k (a wait of
- * the modulated RMSNorm for its row copies), 0x600 + k (a wait of the attention's gradient). */
+ * the modulated RMSNorm for its row copies), 0x600 + k (a wait of the attention's gradient; 0x600 itself:
+ * its shared memory does not start where the kernel needs it). */
 #define MI_DEV_TIMEOUT_GEMM 0x100
 #define MI_DEV_TIMEOUT_ATTN 0x200
 #define MI_DEV_TIMEOUT_SELFTEST 0x300
@@ -363,12 +364,15 @@ mi_status mi_attention_ws(const void* qp, const void* kp, const void* qkv, const
  * mi_qk_norm_rope_backward.  The two backward calls fill disjoint columns of one dqkv
  * [batch * seq, 3H], which is then the gradient of the whole QKV projection's output.  The projection
  * must have stored all of qkv (mi_gemm_bf16, not mi_gemm_bf16_qkv_rope, which leaves out the q and k
- * columns).  batch * seq * n_heads is at most 2^30, seq at most 2^20. */
+ * columns).  seq is at most 2^20, n_heads 1024, and batch * n_heads * seq, with seq rounded up to whole tiles of
+ * 128 rows, 2^30.  A workspace belongs to one call at a time; calls that may overlap need one each. */
 
 /* mi_attention that also stores lse fp32 [batch, heads, seq], the natural logarithm of
  * sum_j exp(q_i k_j / sqrt(128)) over the valid keys (-inf for a row without one, whose output is zero).
  * A masked key's rows of kp and v may hold anything, infinities and NaN included; every row of qp is a
  * query and counts.
+ * Without a mask o has the bytes of mi_attention_ws (mi_attention when ws is NULL); with one, tiles of 128
+ * keys without a valid one are left out on the split schedule, so padding costs nothing there.
  * ws: mi_attention_workspace_size bytes, 256-byte aligned, for the split schedule of mi_attention_ws, or
  * NULL for one CTA per query-tile pair. */
 mi_status mi_attention_lse(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, void* o, float* lse,
@@ -377,7 +381,7 @@ mi_status mi_attention_lse(const void* qp, const void* kp, const void* qkv, cons
 /* Gradient of mi_attention_lse for the output gradient d_o [batch * seq, heads * 128]: dqp, dkp
  * [batch, heads, seq, 128], and dv in columns [2H, 3H) of dqkv [batch * seq, 3H] (its other columns are
  * not written).  o and lse are the forward's; the probabilities are recomputed from lse, so nothing of
- * size seq^2 is stored.  Masked keys get zero gradients, and so do rows without a valid key.  Outputs
+ * size seq^2 is stored.  Masked keys' rows of kp and v may hold anything, as in the forward.  Masked keys get zero gradients, and so do rows without a valid key.  Outputs
  * that overlap an input or each other are refused.  ws: mi_attention_backward_workspace_size bytes,
  * 256-byte aligned; it holds nothing between calls. */
 mi_status mi_attention_backward_workspace_size(int batch, int seq, int n_heads, size_t* bytes);

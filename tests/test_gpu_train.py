@@ -340,6 +340,39 @@ def test_offsets_past_32_bits():
     within(one(c.dv), r["dv"], r["dv_tol"], "dv")
 
 
+def test_binding_refuses_wrong_tensors_on_the_gpu():
+    mi = require_gpu()
+    c = Case(1, 2, 130, None)
+    c.forward(mi)
+    before = c.bits()
+    b, s, h = c.dims
+    ws = torch.empty(mi.attention_backward_workspace_size(b, s, h), dtype=torch.uint8, device="cuda")
+    args = dict(qp=c.q, kp=c.k, qkv=c.qkv, key_mask=None, o=c.o, lse=c.lse, d_o=c.d_o, dqp=c.dq, dkp=c.dk, dqkv=c.dqkv,
+                batch=b, seq=s, n_heads=h, ws=ws)
+    for change, error in ((dict(kp=c.k[:, :, 1:]), ValueError), (dict(lse=c.lse.double()), TypeError),
+                          (dict(d_o=c.d_o.float()), TypeError), (dict(dqp=c.dq.cpu()), ValueError),
+                          (dict(key_mask=torch.ones(b, s + 1, dtype=torch.uint8, device="cuda")), ValueError),
+                          (dict(qkv=c.qkv.T.contiguous().T), ValueError), (dict(ws=ws[:256]), mi.MiError),
+                          (dict(dkp=c.dq), mi.MiError), (dict(dqp=c.q), mi.MiError)):
+        with pytest.raises(error):
+            mi.attention_backward(**{**args, **change})
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(before, c.bits()))  # nothing was enqueued
+    with pytest.raises(mi.MiError, match="overlaps"):
+        mi.attention_lse(c.q, c.k, c.qkv, None, c.q.view(c.o.shape), c.lse, b, s, h)
+
+
+def test_many_elements_of_one_row():
+    """Batches of single rows: one unit each, most of a tile empty; the softmax of one key is 1."""
+    mi = require_gpu()
+    c = Case(700, 3, 1, None)
+    c.mask = torch.ones(700, 1, dtype=torch.uint8, device="cuda")
+    c.mask[::5] = 0
+    c.forward(mi)
+    c.backward(mi)
+    c.check(mi)
+
+
 # ------------------------------------------------------------------------------------ rotary tables
 @pytest.mark.parametrize("rows,pairs,far,scale", [
     (1, (64,), 0.0, 1.0), (16, (32, 32), 0.0, 1.0), (333, (16, 24, 24), 0.0, 0.37), (1000, (1, 62, 1), 1e4, 1.0),

@@ -76,7 +76,8 @@ BWD = dict(qp=P, kp=P + MB, qkv=P + 2 * MB, key_mask=None, o=P + 6 * MB, lse=P +
     (dict(qp=None), 1, "null"), (dict(lse=None), 1, "null"), (dict(dqkv=None), 1, "null"),
     (dict(o=P + 6 * MB + 8), 1, "aligned"), (dict(dkp=P + 10 * MB + 2), 1, "aligned"),
     (dict(batch=0), 1, "positive"), (dict(seq=-1), 1, "positive"), (dict(n_heads=0), 1, "positive"),
-    (dict(seq=(1 << 20) + 1), 2, "2^20"), (dict(n_heads=1025), 2, "1024"), (dict(batch=2048, seq=1 << 18, n_heads=8), 2, "2^30"),
+    (dict(seq=(1 << 20) + 1), 2, "2^20"), (dict(n_heads=1025), 2, "1024"), (dict(batch=2048, seq=1 << 18, n_heads=8), 2, "2^23"), (dict(batch=1 << 21, seq=1, n_heads=8), 2, "2^23"),
+    (dict(batch=2147483647, seq=1 << 20, n_heads=1024), 2, "2^23"),
     (dict(ws=None), 3, "256-byte"), (dict(ws=P + 15 * MB + 16), 3, "256-byte"), (dict(ws_bytes=100), 3, "needed"),
     (dict(dqp=P), 1, "overlaps"), (dict(dkp=P + 9 * MB), 1, "overlaps"), (dict(dqkv=P + 2 * MB + 16), 1, "overlaps"),
     (dict(ws=P + 8 * MB), 1, "overlaps"), (dict(key_mask=P + 10 * MB), 1, "overlaps")])
@@ -131,18 +132,25 @@ def test_workspace_sizes(lib):
     _refused(lib, lib.mi_qk_norm_rope_backward_workspace_size(1, 0, 1, ctypes.byref(n)), 1, "positive")
 
 
-def test_binding_refuses_wrong_sizes():
+def test_binding_refuses_wrong_tensors():
     import diffusion_transformer_denoiser_gb300 as mi
 
     t = torch.empty(10, 64)
     with pytest.raises(ValueError, match="one column per axis"):
         mi.rope_axes_tables(torch.empty(10, 2), (16, 24, 24), t, t)
-    with pytest.raises(ValueError, match="must live on the GPU"):
-        mi.rope_axes_tables(torch.empty(10, 2), (32, 32), t, t)
-    bf = torch.empty(1, 2, 5, 128, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="qp has 1280 elements"):
-        mi.attention_lse(bf, bf, bf, None, bf, bf, 1, 6, 2)
-    with pytest.raises(ValueError, match="qp has 1280 elements"):
-        mi.attention_backward(bf, bf, bf, None, bf, bf, bf, bf, bf, bf, 1, 4, 2, bf)
     with pytest.raises(ValueError, match="too few for 2 tables"):
-        mi.qk_norm_rope_backward(bf, bf, bf, t, t, bf, bf, bf, bf, bf, 2, 5, 2, bf, rope_bstride=640)
+        mi.qk_norm_rope_backward(t, t, t, t, t, t, t, t, t, t, 2, 5, 2, t, rope_bstride=640)
+    for call in (lambda: mi.rope_axes_tables(torch.empty(10, 2), (32, 32), t, t),
+                 lambda: mi.attention_lse(t, t, t, None, t, t, 1, 5, 2),
+                 lambda: mi.attention_backward(t, t, t, None, t, t, t, t, t, t, 1, 5, 2, t),
+                 lambda: mi.qk_norm_rope_backward(t, t, t, t, t, t, t, t, t, t, 1, 5, 2, t)):
+        with pytest.raises(ValueError, match="must live on the GPU"):
+            call()
+    with pytest.raises(ValueError, match="lse has 640 elements, expected 641"):
+        mi._sized(t, torch.float32, 641, "lse", -1)
+    with pytest.raises(ValueError, match="o must live on the GPU of the other tensors, cuda:0"):
+        mi._sized(t, torch.float32, 640, "o", 0)
+    with pytest.raises(TypeError, match="o: expected torch.bfloat16"):
+        mi._sized(t, torch.bfloat16, 640, "o", -1)
+    with pytest.raises(ValueError, match="o must be contiguous"):
+        mi._sized(t.T, torch.float32, 640, "o", -1)
