@@ -22,7 +22,7 @@
 // B operand of the sums.  Roles (384 threads, one CTA per SM):
 //   * warp 0: takes the units (one whose keys are all masked gets its zeros here and is left out) and is
 //     the TMA producer: the CTA's own tiles, the streamed tiles in rings of 2 or 3 stages.
-//   * warp 1: issues the MMAs (convergent warp, one elected lane per instruction).
+//   * warp 1: issues the MMAs (convergent warp, one elected lane).
 //       keys:    dV_n, S_{n+1} | dK_n, dP_{n+1}, each pair behind one wait: P_n (over S_n) and dS_n (over
 //                dP_n) are in the columns that the next scores overwrite, and the MMAs of one thread
 //                execute in order.  P is computed while dK_{n-1}, dP_n run, dS while dV_n, S_{n+1} do.
@@ -37,7 +37,7 @@
 // Both passes are bound by the latency from a tile's scores to its P or dS, and sensitive to the length of
 // the code between: unit ends that are read and stored in rolled loops instead of straight code, and masks
 // that are applied in one place to the packed words, brought the 16418-row gradient from 6.9 to 6.05 ms (in
-// bursts; 6.7 ms at the power cap).  Four warpgroups with a quarter of the columns each, and MMAs issued from
+// bursts; 6.65 ms at the power cap).  Four warpgroups with a quarter of the columns each, and MMAs issued from
 // loops, were slower (6.8 and 6.7 ms in bursts).
 // P and dS are rounded to bf16 once, as matrix operands; scores, D, sums and P in dS are fp32.
 #include "mi_internal.h"
@@ -195,7 +195,7 @@ struct Pass {
   // of the slowest role, so four slots need no release.
   __device__ __forceinline__ int unit(int k) const {
     if (!wait(&bars->unit_full[k & 3], (uint32_t)((k >> 2) & 1), 1)) return -2;
-    return *reinterpret_cast<volatile int*>(&bars->unit[k & 3]);
+    return __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&bars->unit[k & 3]), 0);
   }
   __device__ __forceinline__ void publish(int k, int id) const {
     if (lane == 0) {
@@ -248,31 +248,45 @@ constexpr uint32_t kTile16 = TILE_BYTES >> 4;  // descriptor start addresses cou
 constexpr uint32_t kIdescScores = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdescSum = idesc_bf16(128, 128, false, true);
 
+// The three products, 8 MMAs each behind one election, by a warp whose index and TMEM base the compiler knows to
+// be the same in all lanes (the broadcasts where the kernel begins).  An election for every MMA, without the
+// broadcasts, took 75 instructions per MMA: 100 against 95 us at 3 x 10 heads x 1501, 490 against 477 at 24 x 4130.
+// (With the broadcasts, elections one by one are the slowest: 611 us.)
+
 // D = A B^T over d, both tiles row-major in shared memory.
 __device__ __forceinline__ void scores_ss(uint32_t d, uint64_t a, uint64_t b) {
+  if (elect_one()) {
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t off = ((uint32_t)(kk >> 2) * HALF_BYTES + (uint32_t)(kk & 3) * 32u) >> 4;
-    tc_mma_ss_warp(d, a + off, b + off, kIdescScores, kk > 0 ? 1u : 0u);
+    for (int kk = 0; kk < 8; ++kk) {
+      const uint32_t off = ((uint32_t)(kk >> 2) * HALF_BYTES + (uint32_t)(kk & 3) * 32u) >> 4;
+      tc_mma_ss(d, a + off, b + off, kIdescScores, kk > 0 ? 1u : 0u);
+    }
   }
+  __syncwarp();
 }
 
 // The same with A in TMEM.
 __device__ __forceinline__ void scores_ts(uint32_t d, uint32_t a, uint64_t b) {
+  if (elect_one()) {
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t off = ((uint32_t)(kk >> 2) * HALF_BYTES + (uint32_t)(kk & 3) * 32u) >> 4;
-    tc_mma_ts_warp(d, a + (uint32_t)kk * 8u, b + off, kIdescScores, kk > 0 ? 1u : 0u);
+    for (int kk = 0; kk < 8; ++kk) {
+      const uint32_t off = ((uint32_t)(kk >> 2) * HALF_BYTES + (uint32_t)(kk & 3) * 32u) >> 4;
+      tc_mma_ts(d, a + (uint32_t)kk * 8u, b + off, kIdescScores, kk > 0 ? 1u : 0u);
+    }
   }
+  __syncwarp();
 }
 
 // D (+)= A B over the 128 streamed rows, A (P or dS) in TMEM: the two warpgroups' halves `half_cols` columns
 // apart, B read along its rows.
 __device__ __forceinline__ void sum_ts(uint32_t d, uint32_t a, uint32_t half_cols, uint64_t b, bool first) {
+  if (elect_one()) {
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    tc_mma_ts_warp(d, a + (uint32_t)(kk >> 2) * half_cols + (uint32_t)(kk & 3) * 8u, b + (uint32_t)kk * (2048u >> 4),
-                   kIdescSum, (!first || kk > 0) ? 1u : 0u);
+    for (int kk = 0; kk < 8; ++kk)
+      tc_mma_ts(d, a + (uint32_t)(kk >> 2) * half_cols + (uint32_t)(kk & 3) * 8u, b + (uint32_t)kk * (2048u >> 4),
+                kIdescSum, (!first || kk > 0) ? 1u : 0u);
+  }
+  __syncwarp();
 }
 
 // 64 accumulator columns of a warp's 32 rows, scaled, as bf16 into its 4 KB of the staging tile
@@ -1112,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   c.bars = bars;
   c.abort_flag = &bars->abort_flag;
   c.n_tiles = p.seq_pad / BT;
-  c.warp = threadIdx.x >> 5;
+  c.warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
   c.lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     init_bars(bars, true);
@@ -1131,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  c.tmem = bars->tmem_slot;
+  c.tmem = __shfl_sync(0xffffffffu, bars->tmem_slot, 0);
   grid_dep_wait();
   // (No early launch of the next kernel: this one's CTAs end up to a unit apart, and whatever began to fill the
   // SMs that are done would have to stay there.)

@@ -286,6 +286,13 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
+// True in one lane of a convergent warp, the same one at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Warp-convergent forms: every lane of the issuing warp executes the call and one lane, chosen by
 // elect.sync, issues the operation.  A convergent issuing warp keeps its descriptors and loop
 // state on the uniform datapath and needs few issue slots per MMA, so the tensor pipe stays fed
