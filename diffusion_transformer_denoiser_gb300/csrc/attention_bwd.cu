@@ -34,11 +34,19 @@
 //     rows (queries pass): zero times an infinity or NaN in a padded row would not be zero.
 //   * warps 4-11: two warpgroups, each half of the 128 streamed rows; one thread per lane.  They also read
 //     the accumulators out (queries pass: through shared memory, stored by TMA, a warp its own 32 rows).
-// Both passes are bound by the latency from a tile's scores to its P or dS, and sensitive to the length of
-// the code between: unit ends that are read and stored in rolled loops instead of straight code, and masks
-// that are applied in one place to the packed words, brought the 16418-row gradient from 6.9 to 6.05 ms (in
-// bursts; 6.65 ms at the power cap).  Four warpgroups with a quarter of the columns each, and MMAs issued from
-// loops, were slower (6.8 and 6.7 ms in bursts).
+// Both passes are bound by the latency from a tile's scores to its P or dS, and sensitive to the length of the
+// code (the roles' loops share the SM's instruction cache).  Shorter code was what made them faster, for 24 heads
+// x 4130 rows in bursts (at the power cap that a second of calls reaches, 3 to 9 % more):
+//   * unit ends that are read and stored in rolled loops, and masks applied in one place to the packed words;
+//     then 460 us
+//   * one election for the 8 MMAs of a product (75 instructions per MMA before): 447
+//   * waits with a single poll in the code, and a vote on its answer, where a first test without a vote had
+//     saved the vote: 432
+//   * descriptors made from one word, the producers' loops not unrolled: 424
+// and in the queries pass the loads of dP asked for before the exponentials of S: 418.  Slower: four warpgroups
+// with a quarter of the columns each, MMAs issued from loops, scores read and P stored in halves.  Cutting units
+// along the streamed rows, with fp32 parts that another kernel adds up, pays for a single head of 1000 rows or
+// more (4130: 34 instead of 49 us) and costs from two heads on (2 x 4130: 60 instead of 48), so it is not done.
 // P and dS are rounded to bf16 once, as matrix operands; scores, D, sums and P in dS are fp32.
 #include "mi_internal.h"
 #include "ptx.cuh"
@@ -188,8 +196,17 @@ struct Pass {
   int n_tiles;   // tiles of a sequence
   int warp, lane;
 
+  // Bounded, by a whole warp: one poll in the code, with a vote on its answer.
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int code) const {
-    return mbar_wait_warp(bar, parity, abort_flag, p->err, DEV_TIMEOUT_ATTN_BWD + code);
+    const uint32_t at = smem_u32(bar);
+#pragma unroll 1
+    for (uint32_t it = 0; it < kWaitPolls; ++it) {
+      if (__all_sync(0xffffffffu, mbar_try_wait<false>(at, parity))) return true;
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    }
+    *abort_flag = 1;
+    atomicCAS(p->err, 0, DEV_TIMEOUT_ATTN_BWD + code);
+    return false;
   }
   // The CTA's k-th unit (-1: none); -2 when the CTA was aborted.  The producer is at most two units ahead
   // of the slowest role, so four slots need no release.
@@ -227,6 +244,7 @@ struct Pass {
 
 // Clears the output rows of tile `own` (zeros of a unit without a valid key), by one warp.
 __device__ __forceinline__ void zero_out(__nv_bfloat16* rows, size_t stride, int first, int seq, int lane) {
+#pragma unroll 1
   for (int r = first + (lane >> 4); r < first + BT && r < seq; r += 2)
     *reinterpret_cast<uint4*>(rows + (size_t)r * stride + (lane & 15) * 8) = make_uint4(0, 0, 0, 0);
 }
@@ -248,30 +266,36 @@ constexpr uint32_t kTile16 = TILE_BYTES >> 4;  // descriptor start addresses cou
 constexpr uint32_t kIdescScores = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdescSum = idesc_bf16(128, 128, false, true);
 
+// A tile's descriptor by its low word (address and leading offset); the high word is the same for all.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t start, uint32_t lbo) {
+  return ((start & 0x3FFFFu) >> 4) | (lbo >> 4) << 16;
+}
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return (uint64_t)kDescHi << 32 | lo; }
+
 // The three products, 8 MMAs each behind one election, by a warp whose index and TMEM base the compiler knows to
-// be the same in all lanes (the broadcasts where the kernel begins).  An election for every MMA, without the
-// broadcasts, took 75 instructions per MMA: 100 against 95 us at 3 x 10 heads x 1501, 490 against 477 at 24 x 4130.
-// (With the broadcasts, elections one by one are the slowest: 611 us.)
+// be the same in all lanes (the broadcasts where the kernel begins).  (With the broadcasts and an election for
+// every MMA the kernel is slowest: 611 us at 24 heads x 4130, 490 without either.)
 
 // D = A B^T over d, both tiles row-major in shared memory.
-__device__ __forceinline__ void scores_ss(uint32_t d, uint64_t a, uint64_t b) {
+__device__ __forceinline__ void scores_ss(uint32_t d, uint32_t a, uint32_t b) {
   if (elect_one()) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
       const uint32_t off = ((uint32_t)(kk >> 2) * HALF_BYTES + (uint32_t)(kk & 3) * 32u) >> 4;
-      tc_mma_ss(d, a + off, b + off, kIdescScores, kk > 0 ? 1u : 0u);
+      tc_mma_ss(d, desc(a + off), desc(b + off), kIdescScores, kk > 0 ? 1u : 0u);
     }
   }
   __syncwarp();
 }
 
 // The same with A in TMEM.
-__device__ __forceinline__ void scores_ts(uint32_t d, uint32_t a, uint64_t b) {
+__device__ __forceinline__ void scores_ts(uint32_t d, uint32_t a, uint32_t b) {
   if (elect_one()) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
       const uint32_t off = ((uint32_t)(kk >> 2) * HALF_BYTES + (uint32_t)(kk & 3) * 32u) >> 4;
-      tc_mma_ts(d, a + (uint32_t)kk * 8u, b + off, kIdescScores, kk > 0 ? 1u : 0u);
+      tc_mma_ts(d, a + (uint32_t)kk * 8u, desc(b + off), kIdescScores, kk > 0 ? 1u : 0u);
     }
   }
   __syncwarp();
@@ -279,11 +303,11 @@ __device__ __forceinline__ void scores_ts(uint32_t d, uint32_t a, uint64_t b) {
 
 // D (+)= A B over the 128 streamed rows, A (P or dS) in TMEM: the two warpgroups' halves `half_cols` columns
 // apart, B read along its rows.
-__device__ __forceinline__ void sum_ts(uint32_t d, uint32_t a, uint32_t half_cols, uint64_t b, bool first) {
+__device__ __forceinline__ void sum_ts(uint32_t d, uint32_t a, uint32_t half_cols, uint32_t b, bool first) {
   if (elect_one()) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-      tc_mma_ts(d, a + (uint32_t)(kk >> 2) * half_cols + (uint32_t)(kk & 3) * 8u, b + (uint32_t)kk * (2048u >> 4),
+      tc_mma_ts(d, a + (uint32_t)(kk >> 2) * half_cols + (uint32_t)(kk & 3) * 8u, desc(b + (uint32_t)kk * (2048u >> 4)),
                 kIdescSum, (!first || kk > 0) ? 1u : 0u);
   }
   __syncwarp();
@@ -322,6 +346,7 @@ __device__ __forceinline__ int keys_producer(const Pass& c, const CUtensorMap& t
   const int n_units = c.units();
   // the next unit that has a valid key
   auto settle = [&](int id) {
+#pragma unroll 1
     while (id < n_units) {
       if (p.key_mask == nullptr) return id;
       const int own = id % c.n_tiles, bh = id / c.n_tiles, b = bh / p.n_heads;
@@ -346,6 +371,7 @@ __device__ __forceinline__ int keys_producer(const Pass& c, const CUtensorMap& t
   int id = settle((int)blockIdx.x);
   c.publish(0, id);
   int query = id < 0 ? c.draw_queries() : -1;
+#pragma unroll 1
   for (int k = 0; ok && id >= 0; ++k) {
     const int own = id % c.n_tiles, bh = id / c.n_tiles;
     const int b = bh / p.n_heads, h = bh % p.n_heads;
@@ -359,6 +385,7 @@ __device__ __forceinline__ int keys_producer(const Pass& c, const CUtensorMap& t
       tma_load_3d(c.smem + HALF_BYTES, &tmK, &bars->own_x, 64, own * BT, bh);
     }
     ++nown_x;
+#pragma unroll 1
     for (int t = 0; t < c.n_tiles; ++t) {
       if (nx >= kRingQ && !c.wait(&bars->x_empty[x.st], x.ph ^ 1u, 2)) {
         ok = false;
@@ -410,8 +437,10 @@ __device__ __forceinline__ int keys_producer(const Pass& c, const CUtensorMap& t
   // drain the copies still in flight (the last use of each barrier phase)
   if (nown_x > 0) mbar_wait_drain(&bars->own_x, (uint32_t)((nown_x - 1) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
   if (nown_y > 0) mbar_wait_drain(&bars->own_y, (uint32_t)((nown_y - 1) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+#pragma unroll 1
   for (int j = nx - kRingQ < 0 ? 0 : nx - kRingQ; j < nx; ++j)
     mbar_wait_drain(&bars->x_full[j % kRingQ], (uint32_t)((j / kRingQ) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+#pragma unroll 1
   for (int j = ny - kRingDO < 0 ? 0 : ny - kRingDO; j < ny; ++j)
     mbar_wait_drain(&bars->y_full[j % kRingDO], (uint32_t)((j / kRingDO) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
   return query < 0 ? n_units : query;  // (an aborted CTA has none left)
@@ -421,9 +450,9 @@ __device__ __forceinline__ void keys_mma(const Pass& c) {
   Bars* bars = c.bars;
   const uint32_t tmem = c.tmem;
   const uint32_t sm = smem_u32(c.smem);
-  const uint64_t k_d = sdesc_sw128(sm, 16, 1024), v_d = sdesc_sw128(sm + TILE_BYTES, 16, 1024);
-  const uint64_t q_k = sdesc_sw128(sm + OFF_Q, 16, 1024), do_k = sdesc_sw128(sm + OFF_DO, 16, 1024);
-  const uint64_t q_mn = sdesc_sw128(sm + OFF_Q, HALF_BYTES, 1024), do_mn = sdesc_sw128(sm + OFF_DO, HALF_BYTES, 1024);
+  const uint32_t k_d = desc_lo(sm, 16), v_d = desc_lo(sm + TILE_BYTES, 16);
+  const uint32_t q_k = desc_lo(sm + OFF_Q, 16), do_k = desc_lo(sm + OFF_DO, 16);
+  const uint32_t q_mn = desc_lo(sm + OFF_Q, HALF_BYTES), do_mn = desc_lo(sm + OFF_DO, HALF_BYTES);
   const int last = c.n_tiles - 1;
   int id = c.unit(0);
   bool ok = id >= 0;
@@ -711,6 +740,7 @@ __device__ __forceinline__ void queries_producer(const Pass& c, const CUtensorMa
   Bars* bars = c.bars;
   const int n_units = c.units();
   auto settle = [&](int id) {
+#pragma unroll 1
     while (id < n_units) {
       const int own = id % c.n_tiles, bh = id / c.n_tiles;
       if (c.walked(bh / p.n_heads) > 0) return id;
@@ -725,12 +755,14 @@ __device__ __forceinline__ void queries_producer(const Pass& c, const CUtensorMa
   bool ok = true;
   int id = settle(first);
   c.publish(0, id);
+#pragma unroll 1
   for (int k = 0; ok && id >= 0; ++k) {
     const int own = id % c.n_tiles, bh = id / c.n_tiles;
     const int b = bh / p.n_heads, h = bh % p.n_heads;
     const int count = c.walked(b);
     int next_id = -1;
     int t1 = c.tile(b, 0);
+#pragma unroll 1
     for (int n = 0; n < count; ++n) {
       const int t = t1;
       if (n + 1 < count) t1 = c.tile(b, n + 1);
@@ -778,8 +810,10 @@ __device__ __forceinline__ void queries_producer(const Pass& c, const CUtensorMa
     id = next_id;
   }
   if (nown > 0) mbar_wait_drain(&bars->own_y, (uint32_t)((nown - 1) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+#pragma unroll 1
   for (int j = nx - kRingK < 0 ? 0 : nx - kRingK; j < nx; ++j)
     mbar_wait_drain(&bars->x_full[j % kRingK], (uint32_t)((j / kRingK) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
+#pragma unroll 1
   for (int j = ny - kRingV < 0 ? 0 : ny - kRingV; j < ny; ++j)
     mbar_wait_drain(&bars->y_full[j % kRingV], (uint32_t)((j / kRingV) & 1), p.err, DEV_TIMEOUT_ATTN_BWD + 3);
 }
@@ -788,9 +822,9 @@ __device__ __forceinline__ void queries_mma(const Pass& c) {
   Bars* bars = c.bars;
   const uint32_t tmem = c.tmem;
   const uint32_t sm = smem_u32(c.smem);
-  const uint64_t do_d = sdesc_sw128(sm, 16, 1024);
-  const uint64_t k_k = sdesc_sw128(sm + OFF_K, 16, 1024), v_k = sdesc_sw128(sm + OFF_V, 16, 1024);
-  const uint64_t k_mn = sdesc_sw128(sm + OFF_K, HALF_BYTES, 1024);
+  const uint32_t do_d = desc_lo(sm, 16);
+  const uint32_t k_k = desc_lo(sm + OFF_K, 16), v_k = desc_lo(sm + OFF_V, 16);
+  const uint32_t k_mn = desc_lo(sm + OFF_K, HALF_BYTES);
   int id = c.unit(0);
   bool ok = id >= 0;
   int count = ok ? c.walked(id / c.n_tiles / c.p->n_heads) : 0;
@@ -1015,6 +1049,13 @@ __device__ __forceinline__ void queries_compute(const Pass& c, const CUtensorMap
       tc_fence_before();
       __syncwarp();
       if (c.lane == 0) mbar_arrive(&bars->s_read);
+      if (!c.wait(&bars->dp_full, ph, 12)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      tmem_ld32(t_dp, dp);  // (on their way while the exponentials are taken: 205 us instead of 211 of this pass)
+      tmem_ld32(t_dp + 32, dp + 32);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         float z0, z1;
@@ -1022,13 +1063,6 @@ __device__ __forceinline__ void queries_compute(const Pass& c, const CUtensorMap
         pr[2 * i] = __float_as_uint(ex2_approx(z0));
         pr[2 * i + 1] = __float_as_uint(ex2_approx(z1));
       }
-      if (!c.wait(&bars->dp_full, ph, 12)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      tmem_ld32(t_dp, dp);
-      tmem_ld32(t_dp + 32, dp + 32);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
