@@ -36,7 +36,7 @@
 //     the accumulators out (queries pass: through shared memory, stored by TMA, a warp its own 32 rows).
 // Both passes are bound by the latency from a tile's scores to its P or dS, and sensitive to the length of the
 // code (the roles' loops share the SM's instruction cache).  Shorter code was what made them faster, for 24 heads
-// x 4130 rows in bursts (at the power cap that a second of calls reaches, 3 to 9 % more):
+// x 4130 rows in bursts (at the power cap that a second of calls reaches, 6 to 9 % more):
 //   * unit ends that are read and stored in rolled loops, and masks applied in one place to the packed words;
 //     then 460 us
 //   * one election for the 8 MMAs of a product (75 instructions per MMA before): 447
