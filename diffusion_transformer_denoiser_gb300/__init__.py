@@ -137,9 +137,10 @@ def _check(status: int):
         raise MiError(status, msg.decode() if msg else "")
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, current: Optional[int] = None) -> Optional[int]:
+    """The stream's handle; `current`: the current GPU, where the caller has it already."""
     if stream is None:  # the raw handle: building a Stream object costs as much as a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if current is None else current)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -350,7 +351,7 @@ def rope_axes_tables(positions, axis_pairs, rope_cos, rope_sin, theta=10000.0, s
     d, f32 = _on_current(positions, "positions"), torch.float32
     _check(lib().mi_rope_axes_tables(_sized(positions, f32, rows * n, "positions", d), rows, n, (_I * n)(*axis_pairs), theta,
                                      _sized(rope_cos, f32, rows * 64, "rope_cos", d),
-                                     _sized(rope_sin, f32, rows * 64, "rope_sin", d), _stream(stream)))
+                                     _sized(rope_sin, f32, rows * 64, "rope_sin", d), _stream(stream, d)))
 
 
 def time_advance(t, dt, stream=None):
@@ -426,7 +427,7 @@ def attention_lse(qp, kp, qkv, key_mask, o, lse, batch, seq, n_heads, ws=None, s
         _sized(qp, _BF, n, "qp", d), _sized(kp, _BF, n, "kp", d), _sized(qkv, _BF, 3 * n, "qkv", d),
         None if key_mask is None else _sized(key_mask, torch.uint8, batch * seq, "key_mask", d), _sized(o, _BF, n, "o", d),
         _sized(lse, torch.float32, rows, "lse", d), batch, seq, n_heads,
-        _sized(ws, torch.uint8, ws_bytes, "ws", d) if ws_bytes else None, ws_bytes, _stream(stream)))
+        _sized(ws, torch.uint8, ws_bytes, "ws", d) if ws_bytes else None, ws_bytes, _stream(stream, d)))
 
 
 def attention_backward_workspace_size(batch, seq, n_heads) -> int:
@@ -444,7 +445,7 @@ def attention_backward(qp, kp, qkv, key_mask, o, lse, d_o, dqp, dkp, dqkv, batch
         None if key_mask is None else _sized(key_mask, torch.uint8, batch * seq, "key_mask", d), _sized(o, _BF, n, "o", d),
         _sized(lse, torch.float32, rows, "lse", d), _sized(d_o, _BF, n, "d_o", d), _sized(dqp, _BF, n, "dqp", d),
         _sized(dkp, _BF, n, "dkp", d), _sized(dqkv, _BF, 3 * n, "dqkv", d), batch, seq, n_heads,
-        _sized(ws, torch.uint8, ws.numel(), "ws", d), ws.numel(), _stream(stream)))
+        _sized(ws, torch.uint8, ws.numel(), "ws", d), ws.numel(), _stream(stream, d)))
 
 
 def qk_norm_rope_backward_workspace_size(batch, seq, n_heads) -> int:
@@ -468,7 +469,7 @@ def qk_norm_rope_backward(qkv, q_norm_w, k_norm_w, rope_cos, rope_sin, dqp, dkp,
         _sized(rope_sin, f32, rope_sin.numel(), "rope_sin", d), rope_bstride, _sized(dqp, _BF, n, "dqp", d),
         _sized(dkp, _BF, n, "dkp", d), _sized(dqkv, _BF, 3 * n, "dqkv", d), _sized(dq_norm_w, f32, 128, "dq_norm_w", d),
         _sized(dk_norm_w, f32, 128, "dk_norm_w", d), batch, seq, n_heads, eps,
-        _sized(ws, torch.uint8, ws.numel(), "ws", d), ws.numel(), _stream(stream)))
+        _sized(ws, torch.uint8, ws.numel(), "ws", d), ws.numel(), _stream(stream, d)))
 
 
 def gated_add(x, y, mod, gate_row, out, batch, seq, stream=None):
