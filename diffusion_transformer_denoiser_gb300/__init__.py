@@ -456,7 +456,8 @@ def qk_norm_rope_backward_workspace_size(batch, seq, n_heads) -> int:
 
 def qk_norm_rope_backward(qkv, q_norm_w, k_norm_w, rope_cos, rope_sin, dqp, dkp, dqkv, dq_norm_w, dk_norm_w, batch, seq,
                           n_heads, ws, eps=1e-6, rope_bstride=0, stream=None):
-    """Gradients of qk_norm_rope: the q and k columns of dqkv (its v columns are left alone) and the two gains' (fp32)."""
+    """Gradients of qk_norm_rope: the q and k columns of dqkv (its v columns are left alone) and the two gains' (fp32).
+    Where a head's dqp or dkp is zero in a row, that row's q or k may hold anything: it gets zeros and adds nothing."""
     n = batch * n_heads * seq * 128
     table = (batch - 1) * rope_bstride + seq * 64
     if rope_cos.numel() < table or rope_sin.numel() < table:

@@ -280,11 +280,83 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __nv_bfloat16* 
 // of the row's angles for all of them.  dgain is summed in registers, then over the CTA's warps, then over
 // the CTAs, each in a fixed order: by a second kernel, or (kCluster, few rows) over the one cluster of the
 // launch through shared memory, which saves the second launch where launches are what a call costs.
+// A head whose dy is zero in a row (a masked key's, or a row's without a valid key) has a zero gradient and
+// adds nothing to dgain, whatever x holds; but zero times an infinity or NaN in a padded row is not zero.  Such
+// a row leaves a sum that is not finite, and the warp then takes its items again, leaving such heads out (looked
+// for head by head in the first place it costs 3 to 7 %; a call without such rows takes what it took before).
 constexpr int kQkBwdThreads = 256;
 constexpr int kQkBwdWarps = kQkBwdThreads / 32;
 constexpr int kQkHeads = 4;
 constexpr int kQkCtas = 3;  // per SM
 constexpr int kQkCluster = 8;
+
+// One head of a row: adds to dg and returns dx of this lane's 8 elements.  live: false where x and r count as zero.
+__device__ __forceinline__ uint4 qk_bwd_head(uint4 xv, uint4 yv, const float (&cs)[4], const float (&sn)[4], const float (&g)[8],
+                                             float eps, bool live, float (&dg)[8]) {
+  float x[8], y[8];
+  unpack8(xv, x);
+  unpack8(yv, y);
+#pragma unroll
+  for (int pr = 0; pr < 4; ++pr) {
+    const float a = y[2 * pr], bb = y[2 * pr + 1];
+    y[2 * pr] = fmaf(a, cs[pr], bb * sn[pr]);
+    y[2 * pr + 1] = fmaf(bb, cs[pr], -a * sn[pr]);
+  }
+  float ss = 0.0f, tx = 0.0f;  // sums of x^2 and of t x
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    ss = fmaf(x[e], x[e], ss);
+    tx = fmaf(y[e] * g[e], x[e], tx);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    tx += __shfl_xor_sync(0xffffffffu, tx, o);
+  }
+  const float r = live ? rsqrtf(ss * (1.0f / kHeadDim) + eps) : 0.0f;
+  const float m = tx * r * r * (1.0f / kHeadDim);  // mean(t n) r
+  float o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    dg[e] = fmaf(y[e], x[e] * r, dg[e]);
+    o[e] = r * fmaf(y[e], g[e], -x[e] * m);
+  }
+  return pack8(o);
+}
+
+// A warp's items again, a head at a time; heads whose dy is zero are left out of dgain and get zeros.
+__device__ __forceinline__ void qk_bwd_again(const __nv_bfloat16* qkv, const __nv_bfloat16* gain, const float* cosv,
+                                          const float* sinv, int rope_bstride, const __nv_bfloat16* dyp,
+                                          __nv_bfloat16* dqkv, int batch, int seq, int heads, float eps, float* sum) {
+  const int lane = threadIdx.x & 31;
+  const int e0 = (lane & 15) * 8;
+  const int H = heads * kHeadDim;
+  const int groups = (heads + kQkHeads - 1) / kQkHeads;
+  const long long total = (long long)batch * seq * groups;
+  float g[8], dg[8] = {};
+  unpack8(__ldg(reinterpret_cast<const uint4*>(gain + e0)), g);
+  for (long long item = (long long)blockIdx.x * kQkBwdWarps + (threadIdx.x >> 5); item < total;
+       item += (long long)gridDim.x * kQkBwdWarps) {
+    const long long row = item / groups;
+    const int b = (int)(row / seq), s = (int)(row % seq), h0 = (int)(item % groups) * kQkHeads;
+    const size_t tab = (size_t)b * rope_bstride + (size_t)s * (kHeadDim / 2) + (lane & 15) * 4;
+#pragma unroll 1
+    for (int h = h0; h < h0 + kQkHeads && h < heads; ++h) {
+      const size_t x_at = (size_t)row * 3 * H + (size_t)(lane >> 4) * H + (size_t)h * kHeadDim + e0;
+      uint4 xv = __ldg(reinterpret_cast<const uint4*>(qkv + x_at));
+      const uint4 yv = __ldg(reinterpret_cast<const uint4*>(dyp + (((size_t)b * heads + h) * seq + s) * kHeadDim + e0));
+      const uint32_t bits = (yv.x | yv.y | yv.z | yv.w) & 0x7fff7fffu;  // (a zero of either sign)
+      const bool live = ((__ballot_sync(0xffffffffu, bits != 0) >> (lane & 16)) & 0xffffu) != 0;
+      if (!live) xv = make_uint4(0, 0, 0, 0);
+      const float4 c4 = __ldg(reinterpret_cast<const float4*>(cosv + tab));
+      const float4 s4 = __ldg(reinterpret_cast<const float4*>(sinv + tab));
+      const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+      *reinterpret_cast<uint4*>(dqkv + x_at) = qk_bwd_head(xv, yv, cs, sn, g, eps, live, dg);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = dg[e];
+}
 
 template <bool kCluster>
 __global__ void __launch_bounds__(kQkBwdThreads, kQkCtas)
@@ -333,39 +405,18 @@ __global__ void __launch_bounds__(kQkBwdThreads, kQkCtas)
     const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
     for (int i = 0; i < kQkHeads; ++i) {
-      float x[8], y[8];
-      unpack8(xv[i], x);
-      unpack8(yv[i], y);
-#pragma unroll
-      for (int pr = 0; pr < 4; ++pr) {
-        const float a = y[2 * pr], bb = y[2 * pr + 1];
-        y[2 * pr] = fmaf(a, cs[pr], bb * sn[pr]);
-        y[2 * pr + 1] = fmaf(bb, cs[pr], -a * sn[pr]);
-      }
-      float ss = 0.0f, tx = 0.0f;  // sums of x^2 and of t x
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss = fmaf(x[e], x[e], ss);
-        tx = fmaf(y[e] * g[e], x[e], tx);
-      }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        tx += __shfl_xor_sync(0xffffffffu, tx, o);
-      }
-      const float r = rsqrtf(ss * (1.0f / kHeadDim) + eps);
-      const float m = tx * r * r * (1.0f / kHeadDim);  // mean(t n) r
-      float o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dg[e] = fmaf(y[e], x[e] * r, dg[e]);
-        o[e] = r * fmaf(y[e], g[e], -x[e] * m);
-      }
-      if (h0 + i < heads) *reinterpret_cast<uint4*>(dqkv + x_at + (size_t)i * kHeadDim) = pack8(o);
+      const uint4 dx = qk_bwd_head(xv[i], yv[i], cs, sn, g, eps, true, dg);
+      if (h0 + i < heads) *reinterpret_cast<uint4*>(dqkv + x_at + (size_t)i * kHeadDim) = dx;
     }
   }
+  bool finite = true;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sums[warp][which * 128 + e0 + e] = dg[e];
+  for (int e = 0; e < 8; ++e) finite &= fabsf(dg[e]) <= 3.402823466e38f;
+  float* sum = &sums[warp][which * 128 + e0];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = dg[e];
+  if (!__all_sync(0xffffffffu, finite))
+    qk_bwd_again(qkv, which ? wk : wq, cosv, sinv, rope_bstride, which ? dkp : dqp, dqkv, batch, seq, heads, eps, sum);
   __syncthreads();
   float t = 0.0f;
 #pragma unroll

@@ -392,7 +392,9 @@ mi_status mi_attention_backward(const void* qp, const void* kp, const void* qkv,
 /* Gradient of mi_qk_norm_rope: from dqp, dkp [batch, heads, seq, 128] and the forward's inputs, the q and
  * k columns [0, 2H) of dqkv [batch * seq, 3H] (the v columns are not written) and the gradients of the two
  * gains, dq_norm_w and dk_norm_w, fp32 [128], summed over batch, rows and heads in a fixed order
- * (overwritten, not added to).  Outputs that overlap an input or each other are refused.  ws:
+ * (overwritten, not added to).  A head whose dqp (or dkp) is zero in a row gets a zero gradient there and adds
+ * nothing to the gain's, whatever its q (or k) holds, infinities and NaN included: so it is for masked keys and
+ * for rows without a valid key after mi_attention_backward.  Outputs that overlap an input or each other are refused.  ws:
  * mi_qk_norm_rope_backward_workspace_size bytes, 256-byte aligned; it holds nothing between calls. */
 mi_status mi_qk_norm_rope_backward_workspace_size(int batch, int seq, int n_heads, size_t* bytes);
 mi_status mi_qk_norm_rope_backward(const void* qkv, const void* q_norm_w, const void* k_norm_w, const float* rope_cos,

@@ -1,11 +1,13 @@
 """The training pass's outputs in the 2-norm, which a gradient that is wrong by 2 % does not pass, and calls
 that the element-wise tests leave out: long masks, long gradients, captured masked calls, other streams."""
+import math
+
 import pytest
 import torch
 
 from tests._gpu import require_gpu
-from tests._train import HEAD, attention64, heads_of, within
-from tests._train_norms import agrees_with_difference, close_in_norm, directions, head64
+from tests._train import HEAD, U, attention64, heads_of, within
+from tests._train_norms import agrees_with_difference, close_in_norm, directions, head64, norm_error
 from tests.test_gpu_train import BF, Case, _gen, _normal
 
 pytestmark = pytest.mark.gpu
@@ -174,3 +176,99 @@ def test_qk_gradient_refuses_overlaps():
             mi.qk_norm_rope_backward(**{**a, **change})
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(before, c.outputs()))  # nothing was enqueued
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, torch.finfo(BF).min])
+@pytest.mark.parametrize("batch,heads,seq", [(2, 2, 30), (2, 3, 300), (2, 40, 650)])
+def test_padding_may_hold_anything_in_the_whole_pass(bad, batch, heads, seq):
+    """The k and v columns of padded rows, and every column of an element without a valid key: what they hold
+    reaches no output of the four calls.  The bytes are those of zeros in their place, which are held against
+    64-bit autograd of the whole function, the q, k and v columns each by itself."""
+    mi = require_gpu()
+    gen = _gen(heads * seq)
+    rows, width = batch * seq, heads * HEAD
+    mask = torch.ones(batch, seq, dtype=torch.uint8, device="cuda")
+    mask[0] = 0
+    mask[-1, seq // 5:seq // 2] = 0
+    off = (mask == 0).view(-1, 1)
+    columns = torch.arange(3 * width, device="cuda")
+    padding = (off & (columns >= width)) | (off & (torch.arange(rows, device="cuda") < seq).view(-1, 1))
+    clean = _normal(gen, rows, 3 * width).masked_fill_(padding, 0.0)
+    gains = [_normal(gen, HEAD, std=0.1, mean=1.2) for _ in range(2)]
+    d_o = _normal(gen, rows, width)
+    angle = torch.rand(seq, 64, generator=gen, device="cuda") * 50
+    cos, sin = angle.cos(), angle.sin()
+
+    def whole_pass(qkv):
+        qp, kp = (torch.empty(batch, heads, seq, HEAD, dtype=BF, device="cuda") for _ in range(2))
+        o, lse = torch.empty(rows, width, dtype=BF, device="cuda"), torch.empty(batch, heads, seq, device="cuda")
+        mi.qk_norm_rope(qkv, *gains, cos, sin, qp, kp, batch, seq, heads)
+        ws = torch.empty(mi.attention_workspace_size(batch, seq, heads), dtype=torch.uint8, device="cuda")
+        mi.attention_lse(qp, kp, qkv, mask, o, lse, batch, seq, heads, ws=ws)
+        dqp, dkp, dqkv = torch.empty_like(qp), torch.empty_like(kp), torch.empty_like(qkv)
+        ws = torch.empty(max(mi.attention_backward_workspace_size(batch, seq, heads),
+                             mi.qk_norm_rope_backward_workspace_size(batch, seq, heads)), dtype=torch.uint8, device="cuda")
+        mi.attention_backward(qp, kp, qkv, mask, o, lse, d_o, dqp, dkp, dqkv, batch, seq, heads, ws)
+        dg = [torch.empty(HEAD, device="cuda") for _ in range(2)]
+        mi.qk_norm_rope_backward(qkv, *gains, cos, sin, dqp, dkp, dqkv, *dg, batch, seq, heads, ws)
+        torch.cuda.synchronize()
+        assert mi.device_error() == 0
+        return {"o": o, "lse": lse, "dqkv": dqkv, "dgq": dg[0], "dgk": dg[1]}
+
+    want, got = whole_pass(clean), whole_pass(clean.masked_fill(padding, bad))
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+    assert (got["dqkv"][padding] == 0).all()
+
+    x = clean.double().requires_grad_()
+    g64 = [g.double().requires_grad_() for g in gains]
+    parts = x.view(batch, seq, 3, heads, HEAD).permute(2, 0, 3, 1, 4)
+    c64, s64 = cos.double(), sin.double()
+
+    def turn(t, gain):
+        t = t * torch.rsqrt(t.square().mean(3, keepdim=True) + 1e-6) * gain
+        a, b = t[..., 0::2], t[..., 1::2]
+        return torch.stack([a * c64 - b * s64, a * s64 + b * c64], 4).flatten(3)
+
+    # (element 0 has no output: the sum is over element 1)
+    z = turn(parts[0], g64[0])[1] @ turn(parts[1], g64[1])[1].transpose(1, 2) / math.sqrt(HEAD)
+    z = z.masked_fill((mask[1] == 0)[None, None, :], -math.inf)
+    out = (torch.softmax(z, 2) @ parts[2][1]).permute(1, 0, 2).reshape(seq, width)
+    (out * d_o[seq:].double()).sum().backward()
+    # Roundings on the way to a gradient: q and k (which move the scores, of variance 1.2^4, and enter the last
+    # product), P or dS, o, the gradient of q or k, and of qkv: six of U / sqrt(5) in the mean square, times 1.44
+    # at most, in quadrature 1.6 U; never more than 4 U.
+    for i, name in enumerate(("q", "k", "v")):
+        cols = slice(i * width, (i + 1) * width)
+        err = norm_error(got["dqkv"][:, cols], x.grad[:, cols])
+        assert err <= 4 * U, f"d{name}: {err:.3g}"
+    for i, name in enumerate(("dgq", "dgk")):
+        err = norm_error(got[name], g64[i].grad)
+        assert err <= 4 * U, f"{name}: {err:.3g}"
+
+
+@pytest.mark.parametrize("batch,heads,seq", [(1, 2, 30), (2, 6, 1100)])
+def test_rows_without_a_gradient_add_nothing(batch, heads, seq):
+    """A head whose dq or dk is zero in a row gives a zero gradient and adds nothing to the gains', whatever x
+    holds, with eps 0 too; the other head of the row, and q where k has none, stay as they are."""
+    mi = require_gpu()
+    c = QkCase(batch, heads, seq, 31)
+    for i, bad in enumerate((math.nan, math.inf, -math.inf, 0.0, 3e38)):
+        for which in (0, 1):
+            c.dy[which][-1, -1, 3 * i + which] = -0.0 if i % 2 else 0.0
+            c.qkv.view(batch, seq, 3, heads, HEAD)[-1, 3 * i + which, which, -1] = bad
+    for eps in (1e-6, 0.0):
+        a = c.args(mi)
+        mi.qk_norm_rope_backward(**a, eps=eps)
+        got = c.outputs()
+        clean = QkCase(batch, heads, seq, 31)
+        clean.dy = c.dy
+        mi.qk_norm_rope_backward(**clean.args(mi), eps=eps)
+        want = clean.outputs()
+        assert all(t.isfinite().all() for t in got)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        dx = got[0].view(batch, seq, 3, heads, HEAD)
+        for i in range(5):
+            for which in (0, 1):
+                assert (dx[-1, 3 * i + which, which, -1] == 0).all()
+                assert (dx[-1, 3 * i + which, 1 - which, -1] != 0).any()
