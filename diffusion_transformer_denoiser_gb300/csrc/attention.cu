@@ -81,10 +81,9 @@ constexpr float kRescaleLog2 = 8.0f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
-// Natural-log log-sum-exp of a row from its reference max (base 2) and sum; -inf for an empty row.
-__device__ __forceinline__ float row_lse(float m, float l) {
-  return l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : neg_inf();
-}
+// Natural-log log-sum-exp of a row from its reference max (base 2) and sum; -inf for an empty row (whose max is
+// -inf and whose sum is 0), NaN for a sum of NaN (a row with a score of NaN or +infinity).
+__device__ __forceinline__ float row_lse(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
 
 constexpr int kPartRowFloats = 130;                     // a row's 128 O values, then m and l
 constexpr int kPartTileFloats = 128 * kPartRowFloats;   // one query tile of a part

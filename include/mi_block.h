@@ -368,7 +368,8 @@ mi_status mi_attention_ws(const void* qp, const void* kp, const void* qkv, const
  * 128 rows, 2^30.  A workspace belongs to one call at a time; calls that may overlap need one each. */
 
 /* mi_attention that also stores lse fp32 [batch, heads, seq], the natural logarithm of
- * sum_j exp(q_i k_j / sqrt(128)) over the valid keys (-inf for a row without one, whose output is zero).
+ * sum_j exp(q_i k_j / sqrt(128)) over the valid keys (-inf for a row without one, whose output is zero; NaN for a
+ * row with a score of NaN or +infinity).
  * A masked key's rows of kp and v may hold anything, infinities and NaN included; every row of qp is a
  * query and counts.
  * Without a mask o has the bytes of mi_attention_ws (mi_attention when ws is NULL); with one, tiles of 128

@@ -272,3 +272,22 @@ def test_rows_without_a_gradient_add_nothing(batch, heads, seq):
             for which in (0, 1):
                 assert (dx[-1, 3 * i + which, which, -1] == 0).all()
                 assert (dx[-1, 3 * i + which, 1 - which, -1] != 0).any()
+
+
+@pytest.mark.parametrize("batch,heads,seq,mask", [(1, 2, 300, None), (1, 2, 300, "pad"), (2, 40, 650, "pad"), (2, 40, 650, None)])
+def test_log_sum_exp_of_a_row_that_is_not_a_number(batch, heads, seq, mask):
+    """-inf says that a row has no valid key; a query of NaN, or with an infinity (whose scores are infinities of
+    either sign), has a log-sum-exp of NaN."""
+    mi = require_gpu()
+    c, d = Case(batch, heads, seq, mask), Case(batch, heads, seq, mask)
+    at = [0, 77, 130, seq - 1]
+    c.q[:, :, at[:2]] = math.nan
+    c.q[:, :, at[2:], 5] = math.inf
+    c.forward(mi), d.forward(mi)
+    torch.cuda.synchronize()
+    assert mi.device_error() == 0
+    assert c.lse[:, :, at].isnan().all()
+    o, rest = heads_of(c.o, batch, seq, heads), [i for i in range(seq) if i not in at]
+    assert o[:, :, at].isnan().all()
+    assert torch.equal(c.lse[:, :, rest], d.lse[:, :, rest])
+    assert torch.equal(o[:, :, rest], heads_of(d.o, batch, seq, heads)[:, :, rest])
