@@ -915,13 +915,22 @@ static mi_status check_train_shape(int batch, int seq, int n_heads) {
 
 mi_status mi_attention_lse(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, void* o, float* lse,
                            int batch, int seq, int n_heads, void* ws, size_t ws_bytes, void* stream) {
-  if (!lse) return fail(MI_ERR_INVALID_ARG, "null tensor argument");
-  if (!aligned16(lse)) return fail(MI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  if (!qp || !kp || !qkv || !o || !lse) return fail(MI_ERR_INVALID_ARG, "null tensor argument");
+  if (!aligned16(qp) || !aligned16(kp) || !aligned16(qkv) || !aligned16(o) || !aligned16(lse))
+    return fail(MI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
   mi_status st = check_train_shape(batch, seq, n_heads);
   if (st != MI_OK) return st;
   const size_t rows = (size_t)batch * seq, packed = rows * n_heads * 256;
-  const Span spans[] = {{o, packed}, {lse, rows * n_heads * 4}, {qp, packed}, {kp, packed}, {qkv, 3 * packed}, {key_mask, rows}};
-  if (any_overlap(spans, 2, 6)) return fail(MI_ERR_INVALID_ARG, "an output overlaps another tensor");
+  // The kernels write the part of the workspace that they need while others still read the inputs.
+  size_t used = 0;
+  if (ws != nullptr) {
+    st = mi_attention_workspace_size(batch, seq, n_heads, &used);
+    if (st != MI_OK) return st;
+    used = used < ws_bytes ? used : ws_bytes;
+  }
+  const Span spans[] = {{o, packed}, {lse, rows * n_heads * 4}, {used > 0 ? ws : nullptr, used}, {qp, packed}, {kp, packed},
+                        {qkv, 3 * packed}, {key_mask, rows}};
+  if (any_overlap(spans, 3, 7)) return fail(MI_ERR_INVALID_ARG, "an output or the workspace overlaps another tensor");
   return attention_common(qp, kp, qkv, key_mask, o, lse, batch, seq, n_heads, ws, ws_bytes, ws != nullptr, stream);
 }
 

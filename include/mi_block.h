@@ -375,7 +375,7 @@ mi_status mi_attention_ws(const void* qp, const void* kp, const void* qkv, const
  * Without a mask o has the bytes of mi_attention_ws (mi_attention when ws is NULL); with one, tiles of 128
  * keys without a valid one are left out on the split schedule, so padding costs nothing there.
  * ws: mi_attention_workspace_size bytes, 256-byte aligned, for the split schedule of mi_attention_ws, or
- * NULL for one CTA per query-tile pair. */
+ * NULL for one CTA per query-tile pair.  Outputs or a workspace that overlap an input or each other are refused. */
 mi_status mi_attention_lse(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, void* o, float* lse,
                            int batch, int seq, int n_heads, void* ws, size_t ws_bytes, void* stream);
 
@@ -383,7 +383,7 @@ mi_status mi_attention_lse(const void* qp, const void* kp, const void* qkv, cons
  * [batch, heads, seq, 128], and dv in columns [2H, 3H) of dqkv [batch * seq, 3H] (its other columns are
  * not written).  o and lse are the forward's; the probabilities are recomputed from lse, so nothing of
  * size seq^2 is stored.  Masked keys' rows of kp and v may hold anything, as in the forward.  Masked keys get zero gradients, and so do rows without a valid key.  Outputs
- * that overlap an input or each other are refused.  ws: mi_attention_backward_workspace_size bytes,
+ * or a workspace that overlap an input or each other are refused.  ws: mi_attention_backward_workspace_size bytes,
  * 256-byte aligned; it holds nothing between calls. */
 mi_status mi_attention_backward_workspace_size(int batch, int seq, int n_heads, size_t* bytes);
 mi_status mi_attention_backward(const void* qp, const void* kp, const void* qkv, const uint8_t* key_mask, const void* o,
@@ -395,7 +395,7 @@ mi_status mi_attention_backward(const void* qp, const void* kp, const void* qkv,
  * gains, dq_norm_w and dk_norm_w, fp32 [128], summed over batch, rows and heads in a fixed order
  * (overwritten, not added to).  A head whose dqp (or dkp) is zero in a row gets a zero gradient there and adds
  * nothing to the gain's, whatever its q (or k) holds, infinities and NaN included: so it is for masked keys and
- * for rows without a valid key after mi_attention_backward.  Outputs that overlap an input or each other are refused.  ws:
+ * for rows without a valid key after mi_attention_backward.  Outputs or a workspace that overlap an input or each other are refused.  ws:
  * mi_qk_norm_rope_backward_workspace_size bytes, 256-byte aligned; it holds nothing between calls. */
 mi_status mi_qk_norm_rope_backward_workspace_size(int batch, int seq, int n_heads, size_t* bytes);
 mi_status mi_qk_norm_rope_backward(const void* qkv, const void* q_norm_w, const void* k_norm_w, const float* rope_cos,

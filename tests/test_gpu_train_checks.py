@@ -291,3 +291,30 @@ def test_log_sum_exp_of_a_row_that_is_not_a_number(batch, heads, seq, mask):
     assert o[:, :, at].isnan().all()
     assert torch.equal(c.lse[:, :, rest], d.lse[:, :, rest])
     assert torch.equal(o[:, :, rest], heads_of(d.o, batch, seq, heads)[:, :, rest])
+
+
+@pytest.mark.parametrize("name", ["qp", "kp", "qkv", "key_mask", "o", "lse"])
+def test_forward_refuses_a_workspace_that_overlaps(name):
+    """On the split schedule the kernels write the workspace.  A tensor that begins in its last bytes is refused
+    before anything is enqueued, one right behind it is not; a workspace that no schedule uses may be anywhere."""
+    mi = require_gpu()
+    for batch, heads, seq in ((2, 40, 650), (1, 2, 300)):
+        c = Case(batch, heads, seq, "pad")
+        need = mi.attention_workspace_size(batch, seq, heads)
+        assert (need > 0) == (batch == 2)
+        c.forward(mi)
+        want = [c.o.clone(), c.lse.clone()]
+        call = dict(qp=c.q, kp=c.k, qkv=c.qkv, key_mask=c.mask, o=c.o, lse=c.lse, batch=batch, seq=seq, n_heads=heads)
+        t = call[name]
+        size = t.numel() * t.element_size()
+        room = torch.zeros(need + size, dtype=torch.uint8, device="cuda")
+        if need > 0:
+            with pytest.raises(mi.MiError, match="overlaps"):
+                mi.attention_lse(**{**call, name: room[need - 256:][:size].view(t.dtype).view(t.shape)}, ws=room[:need])
+            torch.cuda.synchronize()
+            assert (room == 0).all()
+        call[name] = room[need:].view(t.dtype).view(t.shape).copy_(t)
+        mi.attention_lse(**call, ws=room[:need] if need > 0 else room[:256])
+        torch.cuda.synchronize()
+        assert mi.device_error() == 0
+        assert torch.equal(call["o"], want[0]) and torch.equal(call["lse"], want[1])
