@@ -1250,6 +1250,9 @@ mi_status mi_rope_axes_tables(const float* positions, int rows, int n_axes, cons
   if (rows <= 0 || rows > (1 << 28)) return fail(MI_ERR_INVALID_ARG, "rows=%d out of range", rows);
   if (n_axes < 1 || n_axes > MI_ROPE_MAX_AXES) return fail(MI_ERR_INVALID_ARG, "n_axes=%d: 1..%d", n_axes, MI_ROPE_MAX_AXES);
   if (!(theta > 1.0f) || !(theta < 3.0e38f)) return fail(MI_ERR_INVALID_ARG, "theta must be finite and above 1");
+  const size_t table = (size_t)rows * 64 * sizeof(float);
+  const Span spans[] = {{rope_cos, table}, {rope_sin, table}, {positions, (size_t)rows * n_axes * sizeof(float)}};
+  if (any_overlap(spans, 2, 3)) return fail(MI_ERR_INVALID_ARG, "a table overlaps the other or the positions");
   mi::RopeAxes f;
   int at = 0;
   for (int a = 0; a < n_axes; ++a) {

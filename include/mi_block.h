@@ -262,7 +262,8 @@ mi_status mi_rope_tables(int text_pad, int grid_h, int grid_w, float theta, floa
  *   positions   device fp32 [rows, n_axes], whole or not, of either sign; up to |position| = 2^24 the
  *               tables are within 3 * 2^-24 of the 64-bit values (a position that is not finite gives NaN)
  *   n_axes      1..MI_ROPE_MAX_AXES
- *   axis_pairs  HOST array of n_axes positive counts that add up to 64 */
+ *   axis_pairs  HOST array of n_axes positive counts that add up to 64
+ * Tables that overlap each other or the positions are refused. */
 #define MI_ROPE_MAX_AXES 8
 mi_status mi_rope_axes_tables(const float* positions, int rows, int n_axes, const int* axis_pairs, float theta,
                               float* rope_cos, float* rope_sin, void* stream);

@@ -1,4 +1,5 @@
-"""The checks of tests/_train_norms.py without a GPU: they take a rounded pass, and nothing that is wrong."""
+"""The checks of tests/_train_norms.py without a GPU: they take a rounded pass, and nothing that is wrong.  Refusals
+made before a device is touched."""
 import math
 
 import pytest
@@ -6,6 +7,7 @@ import torch
 
 from tests._train import attention64
 from tests._train_norms import agrees_with_difference, close_in_norm, directions, head64
+from tests.test_train_cpu import MB, P, _axes, _refused, lib  # noqa: F401
 
 
 def _bf(t):
@@ -69,3 +71,18 @@ def test_one_head_by_chunks_is_the_whole(rounded):
     r = head64(q[1, 0], k[1, 0], v[1, 0], mask[1].nonzero().flatten(), g[1, 0], chunk=64)
     for name in ("o", "lse", "dq", "dk", "dv"):
         assert torch.allclose(r[name], ref[name][1, 0], rtol=1e-10, atol=1e-12), name
+
+
+@pytest.mark.parametrize("change", [
+    dict(cos=P + MB, sin=P + MB), dict(cos=P + MB, sin=P + MB + 10 * 256 - 16), dict(cos=P + MB + 10 * 256 - 16, sin=P + MB),
+    dict(pos=P + MB), dict(pos=P + 2 * MB + 10 * 256 - 4), dict(pos=P + 2 * MB - 10 * 12 + 4)])
+def test_rope_axes_refuses_tables_that_overlap(lib, change):  # noqa: F811
+    _refused(lib, _axes(lib, **change), 1, "overlaps")
+
+
+@pytest.mark.parametrize("change", [dict(cos=P + MB, sin=P + MB + 10 * 256), dict(pos=P + 2 * MB + 10 * 256), dict(pos=P + 2 * MB - 10 * 12)])
+def test_rope_axes_takes_tables_that_touch(lib, change):  # noqa: F811
+    """(Only without a GPU, where the call ends at the device it needs.)"""
+    if torch.cuda.is_available():
+        pytest.skip("would launch on addresses that are not the device's")
+    assert _axes(lib, **change) not in (0, 1), lib.mi_last_error()
