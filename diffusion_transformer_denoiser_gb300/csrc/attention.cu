@@ -68,8 +68,11 @@ constexpr int OFF_MASK = OFF_V + 2 * TILE_BYTES;
 constexpr int kMaskWords = 2048;  // key-validity bitmask held in shared memory: up to 65536 keys
 constexpr int OFF_BAR = OFF_MASK + kMaskWords * 4;
 constexpr int OFF_SEG = OFF_BAR + 256;          // the CTA's segment list (int4 each) and its length
-// training forward with a mask on the split schedule: the elements' key tiles with a valid key
-constexpr int kListTiles = 4096, kListElements = 1280;
+// Training forward with a mask on the split schedule: the elements' key tiles with a valid key.  A schedule has at
+// most kSplitUnits units per SM of kListSms, so that many elements and, with two key tiles (or one) for the 256
+// queries of a unit, twice as many tiles.
+constexpr int kSplitUnits = 8, kListSms = 160;
+constexpr int kListElements = kSplitUnits * kListSms, kListTiles = 2 * kListElements;
 constexpr int OFF_LIST = OFF_SEG + 16 * 16 + 16;
 constexpr int SMEM_TOTAL = OFF_SEG + 16 * 16 + 16 + 1024;
 constexpr int SMEM_TOTAL_LIST = OFF_LIST + kListTiles * 2 + 1024;
@@ -852,8 +855,8 @@ cudaError_t attention_launch(const CUtensorMap& tq, const CUtensorMap& tk, const
 // between SMs that a fixed share cannot (at 16418 rows, 10.3 units per SM, one CTA per unit takes
 // 2.10 ms against 2.33 ms split; at 4130 rows, 2.7 units per SM, split takes 153 µs against 157).
 static bool attention_splits(long long units, int num_sms) {
-  static_assert(8 <= kMaxSegs - 3, "a CTA's share must fit the segment list");
-  return num_sms > 0 && units > num_sms && units <= 8LL * num_sms;
+  static_assert(kSplitUnits <= kMaxSegs - 3, "a CTA's share must fit the segment list");
+  return num_sms > 0 && units > num_sms && units <= (long long)kSplitUnits * num_sms;
 }
 
 int attention_grid(int batch, int seq, int n_heads, int num_sms) {
@@ -872,13 +875,12 @@ size_t attention_count_bytes(int batch, int seq, int n_heads) {
   return ((size_t)units * 2 * sizeof(int) + 255) & ~(size_t)255;
 }
 
-// (Units to split are few, so the list fits: at most 8 per SM of 256 queries each.)
+// (kListSms bounds the elements and the tiles; a GPU of more SMs than GB300's 152 and 8 to spare would walk all tiles.)
 size_t attention_list_bytes(int batch, int seq, int n_heads, int num_sms) {
   const long long units = (long long)batch * n_heads * ((seq + 2 * BQ - 1) / (2 * BQ));
   const int n_kv = (seq + BKV - 1) / BKV;
-  if (!attention_splits(units, num_sms) || num_sms > kPrepareThreads || batch > kListElements ||
-      (long long)batch * n_kv > kListTiles)
-    return 0;
+  static_assert(BQ == BKV && kListSms <= kPrepareThreads && kListTiles < kListPartial, "bounds of the list");
+  if (!attention_splits(units, num_sms) || num_sms > kListSms) return 0;
   ListWorkspace w;
   return list_workspace(nullptr, batch, n_kv, num_sms, &w);
 }

@@ -318,3 +318,19 @@ def test_forward_refuses_a_workspace_that_overlaps(name):
         torch.cuda.synchronize()
         assert mi.device_error() == 0
         assert torch.equal(call["o"], want[0]) and torch.equal(call["lse"], want[1])
+
+
+def test_the_longest_lists_of_key_tiles():
+    """As many elements as the split schedule takes (8 query-tile pairs per SM), two key tiles each; and one more,
+    where every unit has its CTA."""
+    mi = require_gpu()
+    most = 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    for batch in (most, most + 1):
+        assert (mi.attention_workspace_size(batch, 251, 1) > 0) == (batch == most)
+        c = Case(batch, 1, 251, None)
+        c.mask = (torch.rand(batch, 251, generator=_gen(3), device="cuda") < 0.7).to(torch.uint8)
+        c.mask[::3, :128] = 0
+        c.mask[1::3, 120:] = 0
+        c.mask[::7] = 0
+        c.forward(mi)
+        c.check(mi, grads=False)
