@@ -734,7 +734,10 @@ static long long qk_bwd_items(int batch, int seq, int n_heads) {
   return (long long)batch * seq * ((n_heads + kQkHeads - 1) / kQkHeads);
 }
 
-// One cluster for up to 2 turns of its 64 warps; beyond, the whole GPU and a second kernel.
+// One cluster for up to 2 turns of its 64 warps; beyond, the whole GPU and a second kernel.  (Cluster against two
+// kernels, replayed from a graph: 64 items 3.3 against 3.8 us, 96 items 4.5 against 3.8, 256 items 6.9 against 4.2.  Called
+// in turn, where launches are what a call costs: 8.7 against 10.5 at all of these.  So a second turn still pays for
+// calls, and costs a replay less than it saves them; a third and fourth do not.)
 static bool qk_bwd_one_cluster(long long items) { return items <= 2LL * kQkCluster * kQkBwdWarps; }
 
 int qk_norm_rope_bwd_grid(int batch, int seq, int n_heads, int num_sms) {
@@ -754,6 +757,10 @@ cudaError_t qk_norm_rope_bwd_launch(const __nv_bfloat16* qkv, const __nv_bfloat1
   if (qk_bwd_one_cluster(qk_bwd_items(batch, seq, n_heads)))
     return launch_kernel_cluster(qk_norm_rope_bwd_kernel<true>, dim3(grid), dim3(kQkBwdThreads), kQkCluster, s, qkv, wq, wk,
                                  cos, sin, rope_bstride, dqp, dkp, dqkv, partial, dwq, dwk, batch, seq, n_heads, eps);
+  // (Early whatever the number of CTAs, unlike launch_early: the attention's gradient, which it follows, does not let
+  // the next kernel in before its end, so nothing piles up.  Both after 2 x 8 heads x 1000: 44.4 us, 44.6 without; this
+  // kernel again and again 8.2, 8.4 without.  Behind the attention forward, which does let it in, it would lose 10 of
+  // 223 us at 24 heads x 4130.)
   cudaError_t e = launch_kernel(qk_norm_rope_bwd_kernel<false>, dim3(grid), dim3(kQkBwdThreads), 0, s, true, qkv, wq, wk,
                                 cos, sin, rope_bstride, dqp, dkp, dqkv, partial, dwq, dwk, batch, seq, n_heads, eps);
   if (e != cudaSuccess) return e;
@@ -813,6 +820,9 @@ cudaError_t rope_axes_launch(const float* pos, int rows, int n_axes, const RopeA
   const int need = (rows + 15) / 16;
   const int cap = 4 * num_sms;
   const int grid = need < cap ? need : cap;
+  // (Early whatever the number of CTAs, unlike launch_early: alone 2.6 against 3.1 us at 3000 rows, 4.0 against 4.4 at
+  // 9000, 8.8 against 9.3 at 75,826; behind an attention forward of 2 heads x 2 x 500 rows 13.4 against 13.6, 14.7
+  // against 15.5, 19.7 against 20.1, and 0.2 us the other way behind one of 2 x 8 x 1000.)
   return launch_kernel(rope_axes_kernel, dim3(grid), dim3(256), 0, s, true, pos, rows, n_axes, f, cosv, sinv);
 }
 

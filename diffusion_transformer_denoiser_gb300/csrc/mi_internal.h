@@ -171,7 +171,7 @@ cudaError_t time_advance_launch(float* t, int n, float dt, cudaStream_t s);
 // global-memory access.  On unless the environment sets MI_PDL=0 (read once per process).
 bool pdl_enabled();
 
-// Whether a kernel of many small CTAs is launched that way.  CTAs that start while the previous kernel still
+// Whether a kernel of many small CTAs that may follow any other is launched that way.  CTAs that start while the previous kernel still
 // runs pile up on the SMs that it has left and stay there: 256 CTAs of 256 threads behind a kernel whose
 // CTAs end 10 us apart took 9 us longer than without (46 against 37 us for both).  With no more CTAs than
 // SMs the early start wins (2 us of a 7 us call).
