@@ -383,7 +383,9 @@ mi_status mi_attention_lse(const void* qp, const void* kp, const void* qkv, cons
 /* Gradient of mi_attention_lse for the output gradient d_o [batch * seq, heads * 128]: dqp, dkp
  * [batch, heads, seq, 128], and dv in columns [2H, 3H) of dqkv [batch * seq, 3H] (its other columns are
  * not written).  o and lse are the forward's; the probabilities are recomputed from lse, so nothing of
- * size seq^2 is stored.  Masked keys' rows of kp and v may hold anything, as in the forward.  Masked keys get zero gradients, and so do rows without a valid key.  Outputs
+ * size seq^2 is stored.  Masked keys' rows of kp and v may hold anything, as in the
+ * forward.  Masked keys get zero gradients, and so do rows without a valid key.  Every row of qp, o, lse and d_o of an
+ * element with a valid key counts: a padded query adds nothing if its d_o is zero and its q finite.  Outputs
  * or a workspace that overlap an input or each other are refused.  ws: mi_attention_backward_workspace_size bytes,
  * 256-byte aligned; it holds nothing between calls. */
 mi_status mi_attention_backward_workspace_size(int batch, int seq, int n_heads, size_t* bytes);
