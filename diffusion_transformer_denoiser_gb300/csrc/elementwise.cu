@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __nv_bfloat16* 
 // A head whose dy is zero in a row (a masked key's, or a row's without a valid key) has a zero gradient and
 // adds nothing to dgain, whatever x holds; but zero times an infinity or NaN in a padded row is not zero.  Such
 // a row leaves a sum that is not finite, and the warp then takes its items again, leaving such heads out (looked
-// for head by head in the first place it costs 3 to 7 %; a call without such rows takes what it took before).
+// for head by head in the first place it costs every call 3 to 7 %; this way only calls with such rows pay: 118 instead of
+// 53 us at 8260 rows x 24 heads when every warp has some).
 constexpr int kQkBwdThreads = 256;
 constexpr int kQkBwdWarps = kQkBwdThreads / 32;
 constexpr int kQkHeads = 4;
