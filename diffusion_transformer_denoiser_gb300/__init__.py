@@ -20,6 +20,8 @@ __all__ = [
     "device_error", "device_supported", "TENSORS", "TimestepModulation", "rope_tables", "time_advance",
     "rope_axes_tables", "attention_lse", "attention_backward", "attention_backward_workspace_size",
     "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_size",
+    "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_size",
+    "mod_rmsnorm_backward", "mod_rmsnorm_backward_workspace_size", "GradSet",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -70,6 +72,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
 
 _SIGNATURES = {
     "mi_last_error": ([], ctypes.c_char_p),
@@ -110,6 +113,18 @@ _SIGNATURES = {
     "mi_attention_backward": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P], _I),
     "mi_qk_norm_rope_backward_workspace_size": ([_I, _I, _I, ctypes.POINTER(_SZ)], _I),
     "mi_qk_norm_rope_backward": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _SZ, _P], _I),
+    "mi_layer_norm": ([_P, _L, _P, _P, _P, _L, _P, _P, _I, _I, _F, _I, _I, _P], _I),
+    "mi_layer_norm_backward_workspace_size": ([_I, _I, ctypes.POINTER(_SZ)], _I),
+    "mi_layer_norm_backward": ([_P, _L, _P, _L, _P, _P, _P, _P, _L, _P, _L, _P, _P, _I, _I, _I, _I, _P, _SZ, _P], _I),
+    "mi_mod_rmsnorm_backward_workspace_size": ([_I, _I, _I, ctypes.POINTER(_SZ)], _I),
+    "mi_mod_rmsnorm_backward": ([_P, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _F, _P, _SZ, _P], _I),
+    "mi_grads_init": ([ctypes.POINTER(_P), _I, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_L),
+                       ctypes.POINTER(_I)], _I),
+    "mi_grads_destroy": ([_P], None),
+    "mi_grads_workspace_size": ([_P, ctypes.POINTER(_SZ)], _I),
+    "mi_grad_norm": ([_P, _P, _P, _SZ, _P], _I),
+    "mi_grad_clip": ([_P, _F, _P, _P], _I),
+    "mi_grad_clip_norm": ([_P, _F, _P, _P, _SZ, _P], _I),
     "mi_gated_add": ([_P, _P, _P, _I, _P, _I, _I, _I, _P], _I),
     "mi_silu_gate": ([_P, _P, _I, _I, _P], _I),
 }
@@ -180,7 +195,26 @@ def _on_current(t: torch.Tensor, name: str) -> int:
     return device
 
 
+def _rows(t: torch.Tensor, dtype, rows: int, width: int, name: str, device: int):
+    """Address and row stride (elements) of a tensor of `rows` rows of `width`: contiguous, or two-dimensional with
+    rows some way apart."""
+    if t.dim() == 2 and t.shape[0] == rows and t.shape[1] == width and (width == 1 or t.stride(1) == 1):
+        stride = t.stride(0)
+    elif t.numel() != rows * width or t.shape[-1] != width:
+        raise ValueError(f"{name} {tuple(t.shape)}: expected {rows} rows of {width}")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    else:
+        stride = width
+    if t.get_device() != device:
+        raise ValueError(f"{name} must live on the GPU of the other tensors, cuda:{device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    return t.data_ptr(), stride
+
+
 _BF = torch.bfloat16
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 def device_supported() -> bool:
@@ -471,6 +505,152 @@ def qk_norm_rope_backward(qkv, q_norm_w, k_norm_w, rope_cos, rope_sin, dqp, dkp,
         _sized(dkp, _BF, n, "dkp", d), _sized(dqkv, _BF, 3 * n, "dqkv", d), _sized(dq_norm_w, f32, 128, "dq_norm_w", d),
         _sized(dk_norm_w, f32, 128, "dk_norm_w", d), batch, seq, n_heads, eps,
         _sized(ws, torch.uint8, ws.numel(), "ws", d), ws.numel(), _stream(stream, d)))
+
+
+def _norm_types(x, params, name: str) -> int:
+    """mi_dtype of x; params: the first of weight and bias that is given, or None.  Returns both types' codes."""
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"{name}: {x.dtype} is not one of bfloat16, float16, float32")
+    if params is None or params.dtype == x.dtype:
+        return _DTYPES[x.dtype], _DTYPES[x.dtype]
+    if params.dtype != torch.float32:
+        raise TypeError(f"weight and bias: expected {x.dtype} or torch.float32, got {params.dtype}")
+    return _DTYPES[x.dtype], 2
+
+
+def layer_norm(x, weight, bias, out, mean=None, rstd=None, eps=1e-6, stream=None):
+    """out = (x - m) rstd weight + bias over the last axis of x; mean, rstd (fp32, one a row) for layer_norm_backward.
+    x and out: bf16, fp16 or fp32, contiguous or two-dimensional with rows some way apart; weight, bias: x's type or
+    fp32, or None."""
+    d, width = _on_current(x, "x"), x.shape[-1]
+    rows = x.numel() // width if width else 0
+    params = weight if weight is not None else bias
+    dt, pt = _norm_types(x, params, "x")
+    xp, xs = _rows(x, x.dtype, rows, width, "x", d)
+    op, os_ = _rows(out, x.dtype, rows, width, "out", d)
+    f32 = torch.float32
+    _check(lib().mi_layer_norm(
+        xp, xs, None if weight is None else _sized(weight, params.dtype, width, "weight", d),
+        None if bias is None else _sized(bias, params.dtype, width, "bias", d), op, os_,
+        None if mean is None else _sized(mean, f32, rows, "mean", d),
+        None if rstd is None else _sized(rstd, f32, rows, "rstd", d), rows, width, eps, dt, pt, _stream(stream, d)))
+
+
+def layer_norm_backward_workspace_size(rows, width) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().mi_layer_norm_backward_workspace_size(rows, width, ctypes.byref(n)))
+    return n.value
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, residual=None, stream=None):
+    """Gradients of layer_norm: dx (with `residual`, the gradient that comes past the norm, added; dx may be that tensor),
+    and the fp32 sums dweight and dbias (either may be None).  A row whose dy is zero adds nothing, whatever it holds."""
+    d, width = _on_current(dy, "dy"), x.shape[-1]
+    rows, f32 = x.numel() // width if width else 0, torch.float32
+    dt, pt = _norm_types(x, weight, "x")
+    yp, ys = _rows(dy, x.dtype, rows, width, "dy", d)
+    xp, xs = _rows(x, x.dtype, rows, width, "x", d)
+    rp, rs = (None, 0) if residual is None else _rows(residual, x.dtype, rows, width, "residual", d)
+    gp, gs = _rows(dx, x.dtype, rows, width, "dx", d)
+    ws_bytes = 0 if ws is None else ws.numel()
+    _check(lib().mi_layer_norm_backward(
+        yp, ys, xp, xs, None if weight is None else _sized(weight, weight.dtype, width, "weight", d),
+        _sized(mean, f32, rows, "mean", d), _sized(rstd, f32, rows, "rstd", d), rp, rs, gp, gs,
+        None if dweight is None else _sized(dweight, f32, width, "dweight", d),
+        None if dbias is None else _sized(dbias, f32, width, "dbias", d), rows, width, dt, pt,
+        _sized(ws, torch.uint8, ws_bytes, "ws", d) if ws_bytes else None, ws_bytes, _stream(stream, d)))
+
+
+def mod_rmsnorm_backward_workspace_size(batch, seq, hidden) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().mi_mod_rmsnorm_backward_workspace_size(batch, seq, hidden, ctypes.byref(n)))
+    return n.value
+
+
+def mod_rmsnorm_backward(dy, x, mod, shift_row, scale_row, dx, dmod, batch, seq, ws, eps=1e-6, residual=None, stream=None):
+    """Gradients of mod_rmsnorm: dx (with `residual`, the residual stream's gradient, added; dx may be that tensor) and the
+    rows shift_row and scale_row of dmod [batch, 6, hidden] (fp32; its other rows are left alone)."""
+    d, hidden = _on_current(dy, "dy"), x.shape[-1]
+    n = batch * seq * hidden
+    _check(lib().mi_mod_rmsnorm_backward(
+        _sized(dy, _BF, n, "dy", d), _sized(x, _BF, n, "x", d), _sized(mod, _BF, batch * 6 * hidden, "mod", d), shift_row,
+        scale_row, None if residual is None else _sized(residual, _BF, n, "residual", d), _sized(dx, _BF, n, "dx", d),
+        _sized(dmod, torch.float32, batch * 6 * hidden, "dmod", d), batch, seq, hidden, eps,
+        _sized(ws, torch.uint8, ws.numel(), "ws", d), ws.numel(), _stream(stream, d)))
+
+
+class GradSet:
+    """A step's gradients as one vector: contiguous bf16, fp16 or fp32 tensors of any number and size, on one GPU (kept
+    alive here), and the tensors that take them clipped (`outs`; None: in place)."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
+        n = len(grads)
+        if outs is not None and len(outs) != n:
+            raise ValueError(f"{n} gradients and {len(outs)} outs")
+        self._keep = (list(grads), None if outs is None else list(outs))
+        self.device = grads[0].get_device() if n else None
+        for i, g in enumerate(grads):
+            self._look(g, f"grads[{i}]")
+            if outs is not None:
+                self._look(outs[i], f"outs[{i}]")
+                if outs[i].dtype != g.dtype or outs[i].numel() != g.numel():
+                    raise ValueError(f"outs[{i}] must have the type and size of grads[{i}]")
+        h = _P()
+        _check(lib().mi_grads_init(
+            ctypes.byref(h), n, (_P * n)(*[g.data_ptr() for g in grads]),
+            None if outs is None else (_P * n)(*[o.data_ptr() for o in outs]), (_L * n)(*[g.numel() for g in grads]),
+            (_I * n)(*[_DTYPES[g.dtype] for g in grads])))
+        self.handle = h
+
+    def _look(self, t, name):
+        if t.get_device() < 0:
+            raise ValueError(f"{name} must live on the GPU")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} must live on the GPU of the other tensors, cuda:{self.device}")
+        if t.dtype not in _DTYPES:
+            raise TypeError(f"{name}: {t.dtype} is not one of bfloat16, float16, float32")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+    def close(self):
+        if getattr(self, "handle", None):
+            lib().mi_grads_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def workspace_size(self) -> int:
+        n = _SZ(0)
+        _check(lib().mi_grads_workspace_size(self.handle, ctypes.byref(n)))
+        return n.value
+
+    def _norm(self, norm):
+        d = _on_current(norm, "norm")
+        if self.device is not None and self.device != d:
+            raise ValueError(f"norm must live on the GPU of the gradients, cuda:{self.device}")
+        return _sized(norm, torch.float32, 1, "norm", d), d
+
+    def norm(self, norm, ws, stream=None):
+        """norm[0] (fp32, on the device): the 2-norm over all gradients."""
+        p, d = self._norm(norm)
+        _check(lib().mi_grad_norm(self.handle, p, _sized(ws, torch.uint8, ws.numel(), "ws", d) if ws.numel() else None,
+                                  ws.numel(), _stream(stream, d)))
+
+    def clip(self, max_norm, norm, stream=None):
+        """Scales the gradients by min(1, max_norm / (norm[0] + 1e-6)); norm is read on the device."""
+        p, d = self._norm(norm)
+        _check(lib().mi_grad_clip(self.handle, max_norm, p, _stream(stream, d)))
+
+    def clip_norm(self, max_norm, norm, ws, stream=None):
+        """norm and clip in one call."""
+        p, d = self._norm(norm)
+        _check(lib().mi_grad_clip_norm(self.handle, max_norm, p,
+                                       _sized(ws, torch.uint8, ws.numel(), "ws", d) if ws.numel() else None, ws.numel(),
+                                       _stream(stream, d)))
 
 
 def gated_add(x, y, mod, gate_row, out, batch, seq, stream=None):

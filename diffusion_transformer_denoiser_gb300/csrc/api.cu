@@ -2,6 +2,7 @@
 // the launch sequence of a block forward and of a guided denoising step.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1044,6 +1045,376 @@ mi_status mi_qk_norm_rope_backward(const void* qkv, const void* q_norm_w, const 
                                               cb(dqp), cb(dkp), mb(dqkv), dq_norm_w, dk_norm_w, static_cast<float*>(ws),
                                               batch, seq, n_heads, eps, dev->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MI_OK : cuda_fail(e, "qk_norm_rope backward");
+}
+
+namespace {
+
+size_t dtype_size(int dtype) { return dtype == MI_F32 ? 4 : 2; }
+
+// Rows of a tensor in memory: `rows` of them, `bytes` long each, `stride` bytes apart (0: all the same row).
+struct RowSpan {
+  const void* at;
+  size_t rows, bytes, stride;
+  size_t extent() const { return rows == 0 ? 0 : (rows - 1) * stride + bytes; }
+};
+
+bool rows_overlap(const RowSpan& a, const RowSpan& b) {
+  if (a.at == nullptr || b.at == nullptr || a.extent() == 0 || b.extent() == 0) return false;
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
+  if (p >= q + b.extent() || q >= p + a.extent()) return false;
+  if (a.stride == b.stride && a.rows > 1 && b.rows > 1) {  // columns of one buffer that do not touch
+    const size_t d = p <= q ? (q - p) % a.stride : (a.stride - (p - q) % a.stride) % a.stride;
+    if (d >= a.bytes && d + b.bytes <= a.stride) return false;
+  }
+  return true;
+}
+
+// The first n_out spans are outputs: none of them may overlap another span.
+bool any_rows_overlap(const RowSpan* v, int n_out, int n) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (rows_overlap(v[i], v[j])) return true;
+  return false;
+}
+
+mi_status check_norm_shape(int rows, int width) {
+  if (rows < 0) return fail(MI_ERR_INVALID_ARG, "rows must not be negative");
+  if (width <= 0) return fail(MI_ERR_INVALID_ARG, "width must be positive");
+  if (width > MI_NORM_MAX_WIDTH) return fail(MI_ERR_UNSUPPORTED, "width=%d: at most %d", width, MI_NORM_MAX_WIDTH);
+  return MI_OK;
+}
+
+mi_status check_norm_types(int dtype, int param_dtype) {
+  if (dtype != MI_BF16 && dtype != MI_F16 && dtype != MI_F32) return fail(MI_ERR_INVALID_ARG, "dtype=%d is not an mi_dtype", dtype);
+  if (param_dtype != dtype && param_dtype != MI_F32)
+    return fail(MI_ERR_UNSUPPORTED, "param_dtype=%d must be dtype=%d or MI_F32", param_dtype, dtype);
+  return MI_OK;
+}
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Rows of a tensor of the norms: stride in elements, at least width (inputs: or 0).
+mi_status check_rows(const char* name, const void* p, int64_t stride, bool input, int rows, int width, size_t size) {
+  if (rows == 0) return MI_OK;
+  if (!p) return fail(MI_ERR_INVALID_ARG, "null tensor argument (%s)", name);
+  if (!aligned_to(p, size)) return fail(MI_ERR_INVALID_ARG, "%s must be aligned to its elements", name);
+  if (rows > 1 && stride < width && !(input && stride == 0))
+    return fail(MI_ERR_INVALID_ARG, "%s: rows %lld elements apart overlap", name, (long long)stride);
+  if (stride < 0 || stride > (1LL << 40)) return fail(MI_ERR_INVALID_ARG, "%s: bad row stride", name);
+  return MI_OK;
+}
+
+RowSpan row_span(const void* p, int64_t stride, int rows, int width, size_t size) {
+  return {p, (size_t)rows, (size_t)width * size, (size_t)stride * size};
+}
+
+RowSpan span_of(const void* p, size_t bytes) { return {p, 1, bytes, bytes}; }
+
+}  // namespace
+
+mi_status mi_layer_norm(const void* x, int64_t x_stride, const void* weight, const void* bias, void* out, int64_t out_stride,
+                        float* mean, float* rstd, int rows, int width, float eps, int dtype, int param_dtype, void* stream) {
+  mi_status st = check_norm_shape(rows, width);
+  if (st != MI_OK) return st;
+  st = check_norm_types(dtype, param_dtype);
+  if (st != MI_OK) return st;
+  const size_t size = dtype_size(dtype), psize = dtype_size(param_dtype);
+  st = check_rows("x", x, x_stride, true, rows, width, size);
+  if (st != MI_OK) return st;
+  st = check_rows("out", out, out_stride, false, rows, width, size);
+  if (st != MI_OK) return st;
+  if (!aligned_to(weight, psize) || !aligned_to(bias, psize) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return fail(MI_ERR_INVALID_ARG, "weight, bias, mean and rstd must be aligned to their elements");
+  const RowSpan spans[] = {row_span(out, out_stride, rows, width, size), span_of(mean, (size_t)rows * 4),
+                           span_of(rstd, (size_t)rows * 4), row_span(x, x_stride, rows, width, size),
+                           span_of(weight, width * psize), span_of(bias, width * psize)};
+  if (any_rows_overlap(spans, 3, 6)) return fail(MI_ERR_INVALID_ARG, "an output overlaps another tensor");
+  if (!(eps >= 0.0f)) return fail(MI_ERR_INVALID_ARG, "eps must be >= 0");
+  if (rows == 0) return MI_OK;
+  DeviceInfo* dev = nullptr;
+  st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  mi::LayerNormArgs a = {};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.weight = weight;
+  a.bias = bias;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.width = width;
+  a.eps = eps;
+  a.dtype = dtype;
+  a.param_dtype = param_dtype;
+  a.err = dev->err;
+  cudaError_t e = mi::layer_norm_launch(a, dev->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MI_OK : cuda_fail(e, "layer norm");
+}
+
+mi_status mi_layer_norm_backward_workspace_size(int rows, int width, size_t* bytes) {
+  if (!bytes) return fail(MI_ERR_INVALID_ARG, "null output pointer");
+  mi_status st = check_norm_shape(rows, width);
+  if (st != MI_OK) return st;
+  DeviceInfo* dev = nullptr;
+  st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  *bytes = mi::norm_bwd_workspace(1, rows, width, dev->num_sms);
+  return MI_OK;
+}
+
+mi_status mi_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* weight,
+                                 const float* mean, const float* rstd, const void* residual, int64_t residual_stride,
+                                 void* dx, int64_t dx_stride, float* dweight, float* dbias, int rows, int width, int dtype,
+                                 int param_dtype, void* ws, size_t ws_bytes, void* stream) {
+  mi_status st = check_norm_shape(rows, width);
+  if (st != MI_OK) return st;
+  st = check_norm_types(dtype, param_dtype);
+  if (st != MI_OK) return st;
+  const size_t size = dtype_size(dtype), psize = dtype_size(param_dtype);
+  st = check_rows("dy", dy, dy_stride, true, rows, width, size);
+  if (st != MI_OK) return st;
+  st = check_rows("x", x, x_stride, true, rows, width, size);
+  if (st != MI_OK) return st;
+  st = check_rows("dx", dx, dx_stride, false, rows, width, size);
+  if (st != MI_OK) return st;
+  if (residual != nullptr) {
+    st = check_rows("residual", residual, residual_stride, true, rows, width, size);
+    if (st != MI_OK) return st;
+  }
+  if (rows > 0 && (!mean || !rstd)) return fail(MI_ERR_INVALID_ARG, "null tensor argument (mean, rstd)");
+  if (!aligned_to(weight, psize) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(dweight, 4) ||
+      !aligned_to(dbias, 4))
+    return fail(MI_ERR_INVALID_ARG, "weight, mean, rstd, dweight and dbias must be aligned to their elements");
+  const bool in_place = residual == dx && (residual_stride == dx_stride || rows <= 1);
+  const size_t sums = (size_t)width * 4;
+  const RowSpan spans[] = {row_span(dx, dx_stride, rows, width, size), span_of(dweight, sums), span_of(dbias, sums),
+                           span_of(ws, ws_bytes), row_span(dy, dy_stride, rows, width, size),
+                           row_span(x, x_stride, rows, width, size), span_of(weight, width * psize),
+                           span_of(mean, (size_t)rows * 4), span_of(rstd, (size_t)rows * 4),
+                           in_place ? RowSpan{nullptr, 0, 0, 0} : row_span(residual, residual_stride, rows, width, size)};
+  if (any_rows_overlap(spans, 4, 10)) return fail(MI_ERR_INVALID_ARG, "an output or the workspace overlaps another tensor");
+  if (ws == nullptr ? ws_bytes != 0 : (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(MI_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  DeviceInfo* dev = nullptr;
+  st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  const size_t need = mi::norm_bwd_workspace(1, rows, width, dev->num_sms);
+  if (ws_bytes < need) return fail(MI_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  mi::NormBwdArgs a = {};
+  a.dy = dy;
+  a.dy_stride = dy_stride;
+  a.x = x;
+  a.x_stride = x_stride;
+  a.residual = residual;
+  a.residual_stride = residual_stride;
+  a.dx = dx;
+  a.dx_stride = dx_stride;
+  a.weight = weight;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.groups = 1;
+  a.seq = rows;
+  a.width = width;
+  a.dtype = dtype;
+  a.param_dtype = param_dtype;
+  a.partial = static_cast<float*>(ws);
+  a.err = dev->err;
+  cudaError_t e = mi::norm_bwd_launch(a, dev->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MI_OK : cuda_fail(e, "layer norm backward");
+}
+
+static mi_status check_mod_shape(int batch, int seq, int hidden) {
+  if (batch <= 0 || seq <= 0) return fail(MI_ERR_INVALID_ARG, "batch and seq must be positive");
+  if (hidden <= 0 || hidden % 256 != 0 || hidden > 4096)
+    return fail(MI_ERR_UNSUPPORTED, "hidden=%d must be a multiple of 256 and at most 4096", hidden);
+  if ((long long)batch * seq > (1LL << 30)) return fail(MI_ERR_UNSUPPORTED, "batch * seq = %lld: at most 2^30", (long long)batch * seq);
+  return MI_OK;
+}
+
+mi_status mi_mod_rmsnorm_backward_workspace_size(int batch, int seq, int hidden, size_t* bytes) {
+  if (!bytes) return fail(MI_ERR_INVALID_ARG, "null output pointer");
+  mi_status st = check_mod_shape(batch, seq, hidden);
+  if (st != MI_OK) return st;
+  DeviceInfo* dev = nullptr;
+  st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  *bytes = mi::norm_bwd_workspace(batch, seq, hidden, dev->num_sms);
+  return MI_OK;
+}
+
+mi_status mi_mod_rmsnorm_backward(const void* dy, const void* x, const void* mod, int shift_row, int scale_row,
+                                  const void* residual, void* dx, float* dmod, int batch, int seq, int hidden, float eps,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  if (!dy || !x || !mod || !dx || !dmod) return fail(MI_ERR_INVALID_ARG, "null tensor argument");
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(mod) || !aligned16(residual) || !aligned16(dx) || !aligned16(dmod))
+    return fail(MI_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  mi_status st = check_mod_shape(batch, seq, hidden);
+  if (st != MI_OK) return st;
+  if (shift_row < 0 || shift_row > 5 || scale_row < 0 || scale_row > 5) return fail(MI_ERR_INVALID_ARG, "mod rows are 0..5");
+  if (!(eps >= 0.0f)) return fail(MI_ERR_INVALID_ARG, "eps must be >= 0");
+  const size_t rows = (size_t)batch * seq, all = rows * hidden * 2;
+  const Span spans[] = {{dx, all}, {dmod, (size_t)batch * 6 * hidden * 4}, {ws, ws ? ws_bytes : 0}, {dy, all}, {x, all},
+                        {mod, (size_t)batch * 6 * hidden * 2}, {residual == dx ? nullptr : residual, all}};
+  if (any_overlap(spans, 3, 7)) return fail(MI_ERR_INVALID_ARG, "an output or the workspace overlaps another tensor");
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(MI_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
+  DeviceInfo* dev = nullptr;
+  st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  const size_t need = mi::norm_bwd_workspace(batch, seq, hidden, dev->num_sms);
+  if (ws_bytes < need) return fail(MI_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  mi::NormBwdArgs a = {};
+  a.dy = dy;
+  a.x = x;
+  a.residual = residual;
+  a.dx = dx;
+  a.dy_stride = a.x_stride = a.residual_stride = a.dx_stride = hidden;
+  a.weight = cb(mod) + (size_t)scale_row * hidden;
+  a.weight_gstride = 6 * hidden;
+  a.dweight = dmod + (size_t)scale_row * hidden;
+  a.dbias = dmod + (size_t)shift_row * hidden;
+  a.sum_gstride = 6 * hidden;
+  a.groups = batch;
+  a.seq = seq;
+  a.width = hidden;
+  a.eps = eps;
+  a.rms = true;
+  a.dtype = a.param_dtype = MI_BF16;
+  a.partial = static_cast<float*>(ws);
+  a.err = dev->err;
+  cudaError_t e = mi::norm_bwd_launch(a, dev->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MI_OK : cuda_fail(e, "mod_rmsnorm backward");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------ gradient clipping
+struct mi_grads {
+  std::vector<mi::GradTensor> t;  // those that are not empty
+  // Whether [p, p + bytes) touches a tensor of the set.
+  bool touches(const void* p, size_t bytes) const {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    for (const mi::GradTensor& g : t) {
+      const size_t size = dtype_size(g.dtype) * (size_t)g.count;
+      const uintptr_t u = reinterpret_cast<uintptr_t>(g.grad), v = reinterpret_cast<uintptr_t>(g.out);
+      if ((a < u + size && u < a + bytes) || (a < v + size && v < a + bytes)) return true;
+    }
+    return false;
+  }
+};
+
+extern "C" {
+
+static mi_status check_grads(int n, const void* const* grads, void* const* outs, const int64_t* counts, const int* dtypes,
+                             std::vector<mi::GradTensor>* t) {
+  struct Piece {
+    uintptr_t at, end;
+    bool out;
+    int tensor;
+  };
+  std::vector<Piece> pieces;
+  pieces.reserve(2 * (size_t)n);
+  t->reserve(n);
+  for (int i = 0; i < n; ++i) {
+    if (dtypes[i] != MI_BF16 && dtypes[i] != MI_F16 && dtypes[i] != MI_F32)
+      return fail(MI_ERR_INVALID_ARG, "tensor %d: dtype=%d is not an mi_dtype", i, dtypes[i]);
+    if (counts[i] < 0 || counts[i] > (1LL << 40)) return fail(MI_ERR_INVALID_ARG, "tensor %d: bad count", i);
+    if (counts[i] == 0) continue;
+    const void* g = grads[i];
+    void* o = outs ? outs[i] : const_cast<void*>(g);
+    const size_t size = dtype_size(dtypes[i]), bytes = size * (size_t)counts[i];
+    if (!g || !o) return fail(MI_ERR_INVALID_ARG, "tensor %d is null", i);
+    if (!aligned_to(g, size) || !aligned_to(o, size))
+      return fail(MI_ERR_INVALID_ARG, "tensor %d must be aligned to its elements", i);
+    const uintptr_t p = reinterpret_cast<uintptr_t>(g), q = reinterpret_cast<uintptr_t>(o);
+    if (p != q) pieces.push_back({p, p + bytes, false, i});
+    pieces.push_back({q, q + bytes, true, i});
+    t->push_back({g, o, counts[i], dtypes[i]});
+  }
+  // In order of their addresses: an output may begin only behind all that came before, an input behind every output.
+  std::sort(pieces.begin(), pieces.end(), [](const Piece& a, const Piece& b) { return a.at < b.at; });
+  uintptr_t any_end = 0, out_end = 0;
+  for (const Piece& p : pieces) {
+    if (p.at < (p.out ? any_end : out_end))
+      return fail(MI_ERR_INVALID_ARG, "tensor %d: what is written overlaps another tensor (or one is listed twice)", p.tensor);
+    any_end = p.end > any_end ? p.end : any_end;
+    if (p.out) out_end = p.end > out_end ? p.end : out_end;
+  }
+  return MI_OK;
+}
+
+mi_status mi_grads_init(mi_grads** out, int n, const void* const* grads, void* const* outs, const int64_t* counts,
+                        const int* dtypes) {
+  if (!out) return fail(MI_ERR_INVALID_ARG, "null argument");
+  *out = nullptr;
+  if (n < 0) return fail(MI_ERR_INVALID_ARG, "n must not be negative");
+  if (n > 0 && (!grads || !counts || !dtypes)) return fail(MI_ERR_INVALID_ARG, "null argument");
+  mi_grads* set = nullptr;
+  try {
+    set = new mi_grads;
+    const mi_status st = check_grads(n, grads, outs, counts, dtypes, &set->t);
+    if (st != MI_OK) {
+      delete set;
+      return st;
+    }
+  } catch (const std::bad_alloc&) {
+    delete set;
+    return fail(MI_ERR_INVALID_ARG, "host allocation failed");
+  }
+  *out = set;
+  return MI_OK;
+}
+
+void mi_grads_destroy(mi_grads* set) { delete set; }
+
+mi_status mi_grads_workspace_size(const mi_grads* set, size_t* bytes) {
+  if (!set || !bytes) return fail(MI_ERR_INVALID_ARG, "null argument");
+  DeviceInfo* dev = nullptr;
+  mi_status st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  *bytes = mi::grads_workspace(set->t.data(), (int)set->t.size(), dev->num_sms);
+  return MI_OK;
+}
+
+static mi_status run_grads(const mi_grads* set, bool compute, bool clip, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                           void* stream) {
+  if (!set || !norm) return fail(MI_ERR_INVALID_ARG, "null argument");
+  if (!aligned_to(norm, 4)) return fail(MI_ERR_INVALID_ARG, "norm must be 4-byte aligned");
+  if (clip && !(max_norm > 0.0f && max_norm <= 3.402823466e38f))
+    return fail(MI_ERR_INVALID_ARG, "max_norm must be positive and finite");
+  if (ws == nullptr ? ws_bytes != 0 : (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(MI_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const Span v = {norm, 4}, w = {ws, ws ? ws_bytes : 0};
+  const Span both[] = {v, w};
+  if (set->touches(norm, 4) || (ws_bytes > 0 && (set->touches(ws, ws_bytes) || any_overlap(both, 1, 2))))
+    return fail(MI_ERR_INVALID_ARG, "norm or the workspace overlaps another tensor");
+  DeviceInfo* dev = nullptr;
+  mi_status st = require_sm103(&dev);
+  if (st != MI_OK) return st;
+  const int n = (int)set->t.size();
+  if (compute) {
+    const size_t need = mi::grads_workspace(set->t.data(), n, dev->num_sms);
+    if (ws_bytes < need) return fail(MI_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  }
+  cudaError_t e = mi::grads_launch(set->t.data(), n, compute, clip, max_norm, norm, ws, dev->num_sms,
+                                   static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MI_OK : cuda_fail(e, "gradient clipping");
+}
+
+mi_status mi_grad_norm(const mi_grads* set, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  return run_grads(set, true, false, 0.0f, norm, ws, ws_bytes, stream);
+}
+
+mi_status mi_grad_clip(const mi_grads* set, float max_norm, const float* norm, void* stream) {
+  return run_grads(set, false, true, max_norm, const_cast<float*>(norm), nullptr, 0, stream);
+}
+
+mi_status mi_grad_clip_norm(const mi_grads* set, float max_norm, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  return run_grads(set, true, true, max_norm, norm, ws, ws_bytes, stream);
 }
 
 mi_status mi_gated_add(const void* x, const void* y, const void* mod, int gate_row, void* out, int batch, int seq,

@@ -127,6 +127,63 @@ cudaError_t qk_norm_rope_bwd_launch(const __nv_bfloat16* qkv, const __nv_bfloat1
                                     cudaStream_t s);
 int qk_norm_rope_bwd_grid(int batch, int seq, int n_heads, int num_sms);
 
+// Layer norm, its gradient and the modulated RMSNorm's gradient (norms.cu).  dtype and param_dtype are mi_dtype values,
+// strides are in elements.
+struct LayerNormArgs {
+  const void* x;
+  long long x_stride;
+  const void* weight;          // or null: 1
+  const void* bias;            // or null: 0
+  void* out;
+  long long out_stride;
+  float* mean;                 // or null
+  float* rstd;                 // or null
+  int rows, width;
+  float eps;
+  int dtype, param_dtype;
+  int* err;
+};
+cudaError_t layer_norm_launch(const LayerNormArgs& a, int num_sms, cudaStream_t s);
+
+// Rows [g seq, (g + 1) seq) of group g share a weight and have their own column sums (layer norm: one group).
+struct NormBwdArgs {
+  const void* dy;
+  long long dy_stride;
+  const void* x;
+  long long x_stride;
+  const void* residual;        // or null
+  long long residual_stride;
+  void* dx;
+  long long dx_stride;
+  const void* weight;          // group g's at weight + g * weight_gstride; null: 1
+  long long weight_gstride;
+  const float* mean;           // layer norm: the forward's; rms: null
+  const float* rstd;
+  float* dweight;              // sum of dy n, group g's at dweight + g * sum_gstride; or null
+  float* dbias;                // sum of dy, likewise; or null.  Equal to dweight: both are added
+  long long sum_gstride;
+  int groups, seq, width;
+  float eps;                   // rms
+  bool rms;                    // n = x r, weight 1 + w; otherwise layer norm
+  int dtype, param_dtype;
+  float* partial;              // norm_bwd_workspace() bytes
+  int* err;
+};
+size_t norm_bwd_workspace(int groups, int seq, int width, int num_sms);
+cudaError_t norm_bwd_launch(const NormBwdArgs& a, int num_sms, cudaStream_t s);
+
+// Norm and clipping of many tensors (grads.cu).
+struct GradTensor {
+  const void* grad;
+  void* out;
+  long long count;
+  int dtype;                   // mi_dtype
+};
+size_t grads_workspace(const GradTensor* t, int n, int num_sms);
+// norm: computed into `norm` and, with clip, used; without, read from it when clipping.
+cudaError_t grads_launch(const GradTensor* t, int n, bool compute, bool clip, float max_norm, float* norm, void* ws,
+                         int num_sms, cudaStream_t s);
+
 // Rotary tables of tokens with several position axes (elementwise.cu): pair j of a row turns by
 // pos[row, axis[j]] * (hi[j] + lo[j]) full turns.
 struct RopeAxes {

@@ -406,6 +406,82 @@ mi_status mi_qk_norm_rope_backward(const void* qkv, const void* q_norm_w, const 
                                    float* dq_norm_w, float* dk_norm_w, int batch, int seq, int n_heads, float eps,
                                    void* ws, size_t ws_bytes, void* stream);
 
+/* Types of the calls below that take more than one. */
+typedef enum mi_dtype {
+  MI_BF16 = 0,
+  MI_F16 = 1,
+  MI_F32 = 2
+} mi_dtype;
+
+/* Layer norm over the last axis: y = (x - m) rstd * weight + bias with m = mean(x), rstd = (mean((x - m)^2) + eps)^-1/2
+ * of each row.
+ *   x, out      [rows, width] of type `dtype`, rows x_stride and out_stride elements apart (at least width; x_stride
+ *               may be 0: one row for all), each aligned to its elements only
+ *   weight, bias  [width] of type `dtype` or MI_F32 (param_dtype), or NULL: 1 and 0
+ *   mean, rstd  fp32 [rows], for mi_layer_norm_backward, or NULL
+ * 1 <= width <= MI_NORM_MAX_WIDTH; rows may be 0 (nothing happens).  The row's mean is taken off before it is
+ * squared, in fp32, so a row far from zero loses nothing; a row with an infinity or NaN gives NaN.  Outputs that
+ * overlap x, the weights or each other are refused (rows that interleave without touching are fine). */
+#define MI_NORM_MAX_WIDTH 16384
+mi_status mi_layer_norm(const void* x, int64_t x_stride, const void* weight, const void* bias, void* out, int64_t out_stride,
+                        float* mean, float* rstd, int rows, int width, float eps, int dtype, int param_dtype, void* stream);
+
+/* Gradient of mi_layer_norm for dy [rows, width], with n = (x - mean) rstd and g = dy weight:
+ *   dx = residual + rstd (g - mean(g) - n mean(g n)),  dweight = sum over rows of dy n,  dbias = sum over rows of dy
+ *   residual    [rows, width] of type `dtype` or NULL: the gradient that comes past the norm, added before dx's one
+ *               rounding; dx may be the same tensor (same address and stride)
+ *   mean, rstd  the forward's
+ *   dweight, dbias  fp32 [width] (overwritten, not added to; zeros for no rows), either may be NULL
+ * A row whose dy is zero gets dx = residual (or 0) and adds nothing, whatever its x, mean and rstd hold, infinities and
+ * NaN included.  Sums over rows have a fixed order.  Other overlaps of an output or the workspace are refused.
+ * ws: mi_layer_norm_backward_workspace_size bytes, 256-byte aligned; it holds nothing between calls. */
+mi_status mi_layer_norm_backward_workspace_size(int rows, int width, size_t* bytes);
+mi_status mi_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* weight,
+                                 const float* mean, const float* rstd, const void* residual, int64_t residual_stride,
+                                 void* dx, int64_t dx_stride, float* dweight, float* dbias, int rows, int width, int dtype,
+                                 int param_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of mi_mod_rmsnorm for dy [batch * seq, hidden], with r = (mean(x^2) + eps)^-1/2, n = x r and
+ * g = dy (1 + mod[b, scale_row]):
+ *   dx = residual + r (g - n mean(g n)),  dmod[b, scale_row] = sum_s dy n,  dmod[b, shift_row] = sum_s dy
+ *   residual  bf16 [batch * seq, hidden] or NULL: the residual stream's gradient, added before dx's one rounding;
+ *             dx may be the same tensor
+ *   dmod      fp32 [batch, 6, hidden]: those two rows of each element are overwritten, the others left alone (with
+ *             shift_row == scale_row the one row gets both sums added)
+ * Rows whose dy is zero are taken as in mi_layer_norm_backward.  Shapes as for mi_mod_rmsnorm; batch * seq at most 2^30.
+ * Sums over rows have a fixed order.  Other overlaps are refused.
+ * ws: mi_mod_rmsnorm_backward_workspace_size bytes, 256-byte aligned; it holds nothing between calls. */
+mi_status mi_mod_rmsnorm_backward_workspace_size(int batch, int seq, int hidden, size_t* bytes);
+mi_status mi_mod_rmsnorm_backward(const void* dy, const void* x, const void* mod, int shift_row, int scale_row,
+                                  const void* residual, void* dx, float* dmod, int batch, int seq, int hidden, float eps,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* The gradients of a step as one vector: their norm over all tensors, and clipping.  A set lists tensors of any
+ * number, size (0 included) and type, each aligned to its elements only; it holds addresses, no device memory, and can
+ * be used by several threads and streams at once.
+ *   grads   n device pointers, counts[i] elements of type dtypes[i] each (HOST arrays, read during the call)
+ *   outs    n device pointers that take the clipped gradients, of the same sizes and types, or NULL: in place.
+ *           outs[i] may be grads[i].  Tensors of which one would be written through two of them are refused. */
+typedef struct mi_grads mi_grads;
+mi_status mi_grads_init(mi_grads** out, int n, const void* const* grads, void* const* outs, const int64_t* counts,
+                        const int* dtypes);
+void mi_grads_destroy(mi_grads* set);
+mi_status mi_grads_workspace_size(const mi_grads* set, size_t* bytes);
+
+/* norm[0] (device fp32) = sqrt(sum of all squares), rounded once from a sum that is kept in 64 bits: gradients whose
+ * squares leave fp32's range on either side still count.  An infinity gives infinity, a NaN gives NaN.
+ * ws: mi_grads_workspace_size bytes, 256-byte aligned; it holds nothing between calls. */
+mi_status mi_grad_norm(const mi_grads* set, float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* outs = grads * c, c = min(1, max_norm / (norm[0] + 1e-6)) in fp32, each product rounded once.  norm is read from the
+ * device: mi_grad_norm's, or one that the caller has put together from several sets or GPUs.  With c = 1 tensors that are
+ * clipped in place are left as they are.  norm = infinity gives c = 0 (and NaN where a gradient is infinite), a NaN gives
+ * NaN everywhere, so a bad step does not pass unseen.  0 < max_norm < infinity. */
+mi_status mi_grad_clip(const mi_grads* set, float max_norm, const float* norm, void* stream);
+
+/* mi_grad_norm and mi_grad_clip in one call, with the same results. */
+mi_status mi_grad_clip_norm(const mi_grads* set, float max_norm, float* norm, void* ws, size_t ws_bytes, void* stream);
+
 /* out = x + mod[b, gate_row] * y, b = row / seq; x, y, out [batch * seq, hidden].  PR #1528,
  * "What it adds" (the gated add kernel; fp32 arithmetic, one bf16 rounding).  out may equal x. */
 mi_status mi_gated_add(const void* x, const void* y, const void* mod, int gate_row, void* out, int batch,
