@@ -1294,23 +1294,45 @@ mi_status mi_mod_rmsnorm_backward(const void* dy, const void* x, const void* mod
 
 // ------------------------------------------------------------------------------ gradient clipping
 struct mi_grads {
-  std::vector<mi::GradTensor> t;  // those that are not empty
+  std::vector<mi::GradEntry> t;  // those that are not empty
+  mi::GradPlan plan;
   // Whether [p, p + bytes) touches a tensor of the set.
   bool touches(const void* p, size_t bytes) const {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    for (const mi::GradTensor& g : t) {
+    for (const mi::GradEntry& g : t) {
       const size_t size = dtype_size(g.dtype) * (size_t)g.count;
       const uintptr_t u = reinterpret_cast<uintptr_t>(g.grad), v = reinterpret_cast<uintptr_t>(g.out);
       if ((a < u + size && u < a + bytes) || (a < v + size && v < a + bytes)) return true;
     }
     return false;
   }
+  // The tables of the launches: as many tensors as one holds, and items that 32 bits count.
+  void make_plan() {
+    const auto add = [](auto* table, mi::GradEntry e, uint32_t items) {
+      e.first = table->items;
+      table->items += items;
+      table->e[table->n++] = e;
+    };
+    uint64_t all = 0;
+    for (const mi::GradEntry& e : t) all += mi::grad_items(e);
+    plan.small = t.size() <= (size_t)mi::kGradSmall && all <= (1u << 30);
+    for (const mi::GradEntry& e : t) {
+      const uint32_t items = mi::grad_items(e);
+      if (plan.small) {
+        add(&plan.one, e, items);
+        continue;
+      }
+      if (plan.many.empty() || plan.many.back().n == mi::kGradLarge || plan.many.back().items + (uint64_t)items > (1u << 30))
+        plan.many.push_back({});
+      add(&plan.many.back(), e, items);
+    }
+  }
 };
 
 extern "C" {
 
 static mi_status check_grads(int n, const void* const* grads, void* const* outs, const int64_t* counts, const int* dtypes,
-                             std::vector<mi::GradTensor>* t) {
+                             std::vector<mi::GradEntry>* t) {
   struct Piece {
     uintptr_t at, end;
     bool out;
@@ -1333,7 +1355,7 @@ static mi_status check_grads(int n, const void* const* grads, void* const* outs,
     const uintptr_t p = reinterpret_cast<uintptr_t>(g), q = reinterpret_cast<uintptr_t>(o);
     if (p != q) pieces.push_back({p, p + bytes, false, i});
     pieces.push_back({q, q + bytes, true, i});
-    t->push_back({g, o, counts[i], dtypes[i]});
+    t->push_back({g, o, counts[i], 0, dtypes[i]});
   }
   // In order of their addresses: an output may begin only behind all that came before, an input behind every output.
   std::sort(pieces.begin(), pieces.end(), [](const Piece& a, const Piece& b) { return a.at < b.at; });
@@ -1361,6 +1383,7 @@ mi_status mi_grads_init(mi_grads** out, int n, const void* const* grads, void* c
       delete set;
       return st;
     }
+    set->make_plan();
   } catch (const std::bad_alloc&) {
     delete set;
     return fail(MI_ERR_INVALID_ARG, "host allocation failed");
@@ -1376,7 +1399,7 @@ mi_status mi_grads_workspace_size(const mi_grads* set, size_t* bytes) {
   DeviceInfo* dev = nullptr;
   mi_status st = require_sm103(&dev);
   if (st != MI_OK) return st;
-  *bytes = mi::grads_workspace(set->t.data(), (int)set->t.size(), dev->num_sms);
+  *bytes = mi::grads_workspace(set->plan, dev->num_sms);
   return MI_OK;
 }
 
@@ -1395,13 +1418,11 @@ static mi_status run_grads(const mi_grads* set, bool compute, bool clip, float m
   DeviceInfo* dev = nullptr;
   mi_status st = require_sm103(&dev);
   if (st != MI_OK) return st;
-  const int n = (int)set->t.size();
   if (compute) {
-    const size_t need = mi::grads_workspace(set->t.data(), n, dev->num_sms);
+    const size_t need = mi::grads_workspace(set->plan, dev->num_sms);
     if (ws_bytes < need) return fail(MI_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
   }
-  cudaError_t e = mi::grads_launch(set->t.data(), n, compute, clip, max_norm, norm, ws, dev->num_sms,
-                                   static_cast<cudaStream_t>(stream));
+  cudaError_t e = mi::grads_launch(set->plan, compute, clip, max_norm, norm, ws, dev->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MI_OK : cuda_fail(e, "gradient clipping");
 }
 

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <vector>
+
 namespace mi {
 
 constexpr int kMaxDevices = 64;
@@ -141,6 +143,7 @@ struct LayerNormArgs {
   int rows, width;
   float eps;
   int dtype, param_dtype;
+  bool param_vec;              // (set by the launch) the parameters are on 16-byte boundaries
   int* err;
 };
 cudaError_t layer_norm_launch(const LayerNormArgs& a, int num_sms, cudaStream_t s);
@@ -166,23 +169,41 @@ struct NormBwdArgs {
   float eps;                   // rms
   bool rms;                    // n = x r, weight 1 + w; otherwise layer norm
   int dtype, param_dtype;
+  bool param_vec;              // (set by the launch) every group's weight is on a 16-byte boundary
   float* partial;              // norm_bwd_workspace() bytes
   int* err;
 };
 size_t norm_bwd_workspace(int groups, int seq, int width, int num_sms);
 cudaError_t norm_bwd_launch(const NormBwdArgs& a, int num_sms, cudaStream_t s);
 
-// Norm and clipping of many tensors (grads.cu).
-struct GradTensor {
+// Norm and clipping of many tensors (grads.cu).  A launch's tensors are a kernel parameter: tensor i has items
+// [first of i, first of i + 1).
+struct GradEntry {
   const void* grad;
   void* out;
-  long long count;
+  long long count;             // elements, at least one
+  uint32_t first;
   int dtype;                   // mi_dtype
 };
-size_t grads_workspace(const GradTensor* t, int n, int num_sms);
-// norm: computed into `norm` and, with clip, used; without, read from it when clipping.
-cudaError_t grads_launch(const GradTensor* t, int n, bool compute, bool clip, float max_norm, float* norm, void* ws,
-                         int num_sms, cudaStream_t s);
+template <int kEntries>
+struct GradTable {
+  int n;
+  uint32_t items;
+  GradEntry e[kEntries];
+};
+constexpr int kGradSmall = 60;    // 1.9 KB: a launch copies its parameters
+constexpr int kGradLarge = 1000;  // of the 32,764 bytes that a kernel's parameters may have
+struct GradPlan {
+  bool small = true;             // one launch, of the small table
+  GradTable<kGradSmall> one = {};
+  std::vector<GradTable<kGradLarge>> many;
+  size_t launches() const { return small ? (one.items > 0 ? 1 : 0) : many.size(); }
+};
+uint32_t grad_items(const GradEntry& e);
+size_t grads_workspace(const GradPlan& p, int num_sms);
+// compute: the norm goes to `norm`; with clip it is used, without compute it is read from there.
+cudaError_t grads_launch(const GradPlan& p, bool compute, bool clip, float max_norm, float* norm, void* ws, int num_sms,
+                         cudaStream_t s);
 
 // Rotary tables of tokens with several position axes (elementwise.cu): pair j of a row turns by
 // pos[row, axis[j]] * (hi[j] + lo[j]) full turns.
