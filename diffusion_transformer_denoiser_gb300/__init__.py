@@ -190,7 +190,7 @@ def _on_current(t: torch.Tensor, name: str) -> int:
     device = t.get_device()
     if device < 0:
         raise ValueError(f"{name} must live on the GPU")
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():  # (a tensor on a GPU: CUDA is up, which is what current_device() sees to)
         raise ValueError(f"{name} lives on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
     return device
 
@@ -198,19 +198,17 @@ def _on_current(t: torch.Tensor, name: str) -> int:
 def _rows(t: torch.Tensor, dtype, rows: int, width: int, name: str, device: int):
     """Address and row stride (elements) of a tensor of `rows` rows of `width`: contiguous, or two-dimensional with
     rows some way apart."""
-    if t.dim() == 2 and t.shape[0] == rows and t.shape[1] == width and (width == 1 or t.stride(1) == 1):
-        stride = t.stride(0)
-    elif t.numel() != rows * width or t.shape[-1] != width:
+    if t.shape[-1] != width or t.numel() != rows * width:
         raise ValueError(f"{name} {tuple(t.shape)}: expected {rows} rows of {width}")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
-    else:
-        stride = width
     if t.get_device() != device:
         raise ValueError(f"{name} must live on the GPU of the other tensors, cuda:{device}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    return t.data_ptr(), stride
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    if t.dim() != 2 or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    return t.data_ptr(), t.stride(0)
 
 
 _BF = torch.bfloat16
@@ -589,17 +587,23 @@ class GradSet:
             raise ValueError(f"{n} gradients and {len(outs)} outs")
         self._keep = (list(grads), None if outs is None else list(outs))
         self.device = grads[0].get_device() if n else None
-        for i, g in enumerate(grads):
-            self._look(g, f"grads[{i}]")
-            if outs is not None:
-                self._look(outs[i], f"outs[{i}]")
-                if outs[i].dtype != g.dtype or outs[i].numel() != g.numel():
-                    raise ValueError(f"outs[{i}] must have the type and size of grads[{i}]")
+        every = self._keep[0] + (self._keep[1] or [])
+        sizes, types = [g.numel() for g in grads], [g.dtype for g in grads]
+        # one look at all of them; what is wrong with which is found out only if something is
+        if (n and self.device < 0) or any(t.get_device() != self.device or not t.is_contiguous() for t in every) \
+                or not set(types) <= _DTYPES.keys() \
+                or (outs is not None and ([o.numel() for o in outs] != sizes or [o.dtype for o in outs] != types)):
+            for i, g in enumerate(grads):
+                self._look(g, f"grads[{i}]")
+                if outs is not None:
+                    self._look(outs[i], f"outs[{i}]")
+                    if outs[i].dtype != g.dtype or outs[i].numel() != g.numel():
+                        raise ValueError(f"outs[{i}] must have the type and size of grads[{i}]")
         h = _P()
         _check(lib().mi_grads_init(
             ctypes.byref(h), n, (_P * n)(*[g.data_ptr() for g in grads]),
-            None if outs is None else (_P * n)(*[o.data_ptr() for o in outs]), (_L * n)(*[g.numel() for g in grads]),
-            (_I * n)(*[_DTYPES[g.dtype] for g in grads])))
+            None if outs is None else (_P * n)(*[o.data_ptr() for o in outs]), (_L * n)(*sizes),
+            (_I * n)(*[_DTYPES[t] for t in types])))
         self.handle = h
 
     def _look(self, t, name):

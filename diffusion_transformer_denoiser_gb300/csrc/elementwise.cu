@@ -756,7 +756,7 @@ cudaError_t qk_norm_rope_bwd_launch(const __nv_bfloat16* qkv, const __nv_bfloat1
                                     cudaStream_t s) {
   const int grid = qk_norm_rope_bwd_grid(batch, seq, n_heads, num_sms);
   if (qk_bwd_one_cluster(qk_bwd_items(batch, seq, n_heads)))
-    return launch_kernel_cluster(qk_norm_rope_bwd_kernel<true>, dim3(grid), dim3(kQkBwdThreads), kQkCluster, s, qkv, wq, wk,
+    return launch_kernel_cluster(qk_norm_rope_bwd_kernel<true>, dim3(grid), dim3(kQkBwdThreads), 0, kQkCluster, s, qkv, wq, wk,
                                  cos, sin, rope_bstride, dqp, dkp, dqkv, partial, dwq, dwk, batch, seq, n_heads, eps);
   // (Early whatever the number of CTAs, unlike launch_early: the attention's gradient, which it follows, does not let
   // the next kernel in before its end, so nothing piles up.  Both after 2 x 8 heads x 1000: 44.4 us, 44.6 without; this

@@ -1,0 +1,165 @@
+// Layer norm.  What it shares with the gradients, and what bounds it, is in norm_rows.cuh.
+#include "norm_rows.cuh"
+
+namespace mi {
+
+namespace {
+
+// A row's sum of squares is taken around its mean, so a row far from zero loses nothing: a warp with n columns finds their
+// mean m and the squares q around it.  Over the warps of a row, A = sum n (m - m_0) and B = sum (q + n (m - m_0)^2) give the
+// row's mean m_0 + A / width and its squares B - A^2 / width.  (What that difference takes off is at most as many times what is
+// left as there are warps, 16: the row's squares are at least n_0 (m_0 - mean)^2, its first warp's.)
+template <typename T, int V, int E, int kDepth, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerNormArgs a, const Plan p) {
+  using P = Piece<T, V>;
+  using L = typename P::L;
+  constexpr int C = E / V, N = P::N, kThreads = kWarps * 32;
+  using In = Reader<T, V, C, kDepth, kWarps>;
+  constexpr int kStage = In::kTurn;
+  extern __shared__ __align__(128) uint8_t memory[];
+  __shared__ float2 parts[2][kWarps + 16];  // a warp's mean and squares (read 16 from a group's first on)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Place<V, C> me(p);
+  const bool wide = p.row_warps > 1;
+  grid_dep_wait();
+  const long long row0 = (long long)a.rows * blockIdx.x / gridDim.x;
+  const int rows = (int)((long long)a.rows * (blockIdx.x + 1) / gridDim.x - row0);
+  const int apart = p.apart;
+  int left = me.group < p.groups ? rows - me.group * p.batch : 0;  // rows from the group's next batch on
+  long long row = row0 + me.group * p.batch + me.sub;
+  uint32_t bytes[C];  // of the thread's pieces that are in the row
+#pragma unroll
+  for (int c = 0; c < C; ++c) bytes[c] = (uint32_t)min(max(a.width - me.column(c), 0), V) * sizeof(T);
+  In x_in(a.x, a.x_stride, row, a.width, me);
+  const uint32_t slot0 = In::place(smem_u32(memory), me);
+  int to_ask = left - me.sub;  // rows of this thread
+  auto ask = [&](uint32_t to) {
+    x_in.ask(a.x, to, me, bytes, to_ask > 0, p.step[0]);
+    to_ask -= apart;
+    copy_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth - 1; ++k) ask(slot0 + k * kStage);
+  grid_dep_launch();
+  const float inv = 1.0f / (float)a.width;
+  auto columns_of = [&](int w) {  // of warp w of a row
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) n += min(max(a.width - (w * C + c) * 32 * V, 0), 32 * V);
+    return (float)n;
+  };
+  const float inv_cols = wide ? 1.0f / fmaxf(columns_of(me.row_warp), 1.0f) : inv;
+  const float n_of_lane = (lane & 15) < p.row_warps ? columns_of(lane & 15) : 0.0f;
+  L w[C][N], b[C][N];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    load_param<T, V>(a.weight, a.param_dtype, a.param_vec, 0, me.column(c), a.width, 1.0f, 0.0f, w[c]);
+    load_param<T, V>(a.bias, a.param_dtype, a.param_vec, 0, me.column(c), a.width, 0.0f, 0.0f, b[c]);
+  }
+  uint8_t* out = static_cast<uint8_t*>(a.out) + (row * a.out_stride + me.first) * (long long)sizeof(T);
+  const uint32_t last = slot0 + (kDepth - 1) * kStage;
+  uint32_t stage = slot0, ahead = last;
+  for (int turn = 0; left > 0; turn ^= 1) {
+    if (V < 4) __syncwarp();  // (the warp has read what now makes room)
+    ask(ahead);
+    copy_wait<kDepth - 1>();
+    if (V < 4) __syncwarp();
+    L x[C][N];
+    L t = v_of<L>(0.0f);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      x_in.load(stage, me, c, p.step[0], x[c]);
+#pragma unroll
+      for (int e = 0; e < N; ++e) t = v_add(t, x[c][e]);
+    }
+    const float s = wide ? warp_sum(v_sum(t)) : lanes_sum(v_sum(t), p.row_lanes);
+    const float m = s * inv_cols;
+    t = v_of<L>(0.0f);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const L nm = bytes[c] == V * sizeof(T) ? v_of<L>(-m) : V == 2 && bytes[c] == sizeof(T) ? v_of2<L>(-m, 0.0f) : v_of<L>(0.0f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const L d = v_add(x[c][e], nm);
+        t = v_fma(d, d, t);
+      }
+    }
+    float mean = m, square = wide ? warp_sum(v_sum(t)) : lanes_sum(v_sum(t), p.row_lanes);
+    if (wide) {
+      if (lane == 0) parts[turn][warp] = make_float2(m, square);
+      group_sync(me.group, p.row_warps);
+      const float first = parts[turn][me.group * p.row_warps].x;
+      const float2 part = parts[turn][me.group * p.row_warps + (lane & 15)];
+      const float d = part.x - first, nd = n_of_lane * d;
+      const float v = lane < 16 ? nd : fmaf(nd, d, part.y);
+      const float2 both = warps_sum2((lane & 15) < p.row_warps ? v : 0.0f);
+      mean = fmaf(both.x, inv, first);
+      square = fmaf(-both.x * inv, both.x, both.y);
+    }
+    const float rstd = rsqrtf(fmaf(square, inv, a.eps));
+    const bool mine = me.sub < left;
+    const L nm = v_of<L>(-mean), rs = v_of<L>(rstd);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      L o[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = v_fma(v_mul(v_add(x[c][e], nm), rs), w[c][e], b[c][e]);
+      if (bytes[c] != 0 && mine) P::store(out + c * me.apart * (int)sizeof(T), bytes[c], o);
+    }
+    if (me.first == 0 && mine) {
+      if (a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    left -= apart;
+    row += apart;
+    out += p.step[3];
+    stage = stage == last ? slot0 : stage + kStage;
+    ahead = ahead == last ? slot0 : ahead + kStage;
+  }
+  copy_wait<0>();
+}
+
+template <typename T, int V, int E, int kWarps>
+cudaError_t layer_norm_run(const LayerNormArgs& a, int num_sms, cudaStream_t s) {
+  constexpr int kTurn = Reader<T, V, E / V, 1, kWarps>::kTurn, kDepth = depth_of(1, kTurn);
+  constexpr auto kKernel = layer_norm_kernel<T, V, E, kDepth, kWarps>;
+  Plan p = make_plan(a.width, V, E, kWarps);
+  p.step[0] = p.apart * a.x_stride * (long long)sizeof(T);
+  p.step[3] = p.apart * a.out_stride * (long long)sizeof(T);
+  const long long need = ((long long)a.rows + p.apart - 1) / p.apart;
+  const int grid = need < num_sms ? (int)need : num_sms;
+  cudaError_t e = allow_ring<kKernel>();
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kKernel, dim3(grid), dim3(kWarps * 32), (size_t)kDepth * kTurn, s, true, a, p);
+}
+
+// Columns of a lane: 16 (40 M bf16 elements: 31 us at width 256, 35 at 2560, 34 at 4096; with 8 and 24 warps 34, 43, 47), but 8
+// in odd rows while a CTA of 24 warps holds two of them (20 M: 49 against 50 us at width 1023, 51 against 49 at 2047), and 32
+// where 16 warps of 16 columns a lane do not hold a row.
+template <typename T, int V>
+cudaError_t layer_norm_any(const LayerNormArgs& a, int num_sms, cudaStream_t s) {
+  if (a.width > 16 * 32 * 16) return layer_norm_run<T, V, 32, 16>(a, num_sms, s);
+  if constexpr (V < 4)
+    if (a.width <= 12 * 32 * 8 / 2) return layer_norm_run<T, V, 8, 24>(a, num_sms, s);
+  return layer_norm_run<T, V, 16, 16>(a, num_sms, s);
+}
+
+template <typename T, int V>
+cudaError_t layer_norm_type(LayerNormArgs a, int num_sms, cudaStream_t s) {
+  a.param_vec = on16(a.weight, 0) && on16(a.bias, 0);
+  const long long size = sizeof(T);
+  if (a.width % V == 0 && on16(a.x, a.x_stride * size) && on16(a.out, a.out_stride * size))
+    return layer_norm_any<T, V>(a, num_sms, s);
+  return layer_norm_any<T, sizeof(T) == 4 ? 1 : 2>(a, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t layer_norm_launch(const LayerNormArgs& a, int num_sms, cudaStream_t s) {
+  if (a.rows <= 0) return cudaSuccess;
+  if (a.dtype == MI_F32) return layer_norm_type<float, 4>(a, num_sms, s);
+  if (a.dtype == MI_F16) return layer_norm_type<__half, 8>(a, num_sms, s);
+  return layer_norm_type<__nv_bfloat16, 8>(a, num_sms, s);
+}
+
+}  // namespace mi

@@ -129,7 +129,7 @@ cudaError_t qk_norm_rope_bwd_launch(const __nv_bfloat16* qkv, const __nv_bfloat1
                                     cudaStream_t s);
 int qk_norm_rope_bwd_grid(int batch, int seq, int n_heads, int num_sms);
 
-// Layer norm, its gradient and the modulated RMSNorm's gradient (norms.cu).  dtype and param_dtype are mi_dtype values,
+// Layer norm (layer_norm.cu), its gradient and the modulated RMSNorm's gradient (norm_bwd.cu).  dtype and param_dtype are mi_dtype values,
 // strides are in elements.
 struct LayerNormArgs {
   const void* x;
@@ -271,13 +271,14 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// The same for a kernel whose CTAs form clusters (no dynamic shared memory).
+// The same for a kernel whose CTAs form clusters.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, unsigned cluster, cudaStream_t s,
+cudaError_t launch_kernel_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, unsigned cluster, cudaStream_t s,
                                   Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

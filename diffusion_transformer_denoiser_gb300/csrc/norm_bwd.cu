@@ -1,0 +1,396 @@
+// Gradients of layer norm and of the modulated RMSNorm.  What they share with the forward, and what bounds them, is in
+// norm_rows.cuh.
+#include "norm_rows.cuh"
+
+namespace mi {
+
+namespace {
+
+constexpr float kMax = 3.402823466e38f;
+constexpr int kCluster = 8;       // CTAs that sum their rows up in one launch, where rows are few
+constexpr int kClusterTurns = 2;  // turns of their groups up to which that is done
+
+// With g = dy w, n = (x - mean) rstd (rms: x rstd) and the row's sums of g and g (x - mean) (rms: of x^2 and g x):
+//   dx = residual + rstd (g - mean(g) - n mean(g n))   (rms: without mean(g))
+//   sums over rows: dweight += dy n, dbias += dy.
+// A row whose sums or statistics are not finite is looked at again: if its dy is zero it counts as absent (so what
+// padding holds reaches nothing), which costs rows that are finite nothing.
+template <typename T, int V, int E, int kDepth, int kWarps, bool kRms, bool kResidual>
+__global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdArgs a, const Plan p, int n_parts) {
+  using P = Piece<T, V>;
+  using L = typename P::L;
+  constexpr int C = E / V, N = P::N, kInputs = kResidual ? 3 : 2, kThreads = kWarps * 32;
+  constexpr bool kHold = E <= 16;  // a row in registers; wider rows are read from shared memory again, their weights from L1
+  using In = Reader<T, V, C, kDepth, kWarps>;
+  constexpr int kStage = kInputs * In::kTurn;
+  extern __shared__ __align__(128) uint8_t memory[];
+  __shared__ float2 parts[2][kWarps + 16];  // a warp's sums (read 16 from a group's first on)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Place<V, C> me(p);
+  const bool wide = p.row_warps > 1;
+  grid_dep_wait();
+  const int set = blockIdx.x / n_parts, part_of_set = blockIdx.x - set * n_parts;
+  const long long row0 = (long long)set * a.seq + (long long)a.seq * part_of_set / n_parts;
+  const int rows = (int)((long long)set * a.seq + (long long)a.seq * (part_of_set + 1) / n_parts - row0);
+  const int apart = p.apart;
+  int left = me.group < p.groups ? rows - me.group * p.batch : 0;  // rows from the group's next batch on
+  long long row = row0 + me.group * p.batch + me.sub;
+  uint32_t bytes[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) bytes[c] = (uint32_t)min(max(a.width - me.column(c), 0), V) * sizeof(T);
+  In x_in(a.x, a.x_stride, row, a.width, me), y_in(a.dy, a.dy_stride, row, a.width, me), r_in(a.residual, a.residual_stride, row, a.width, me);
+  const uint32_t slot0 = In::place(smem_u32(memory), me);
+  int to_ask = left - me.sub;
+  auto ask = [&](uint32_t to) {
+    x_in.ask(a.x, to, me, bytes, to_ask > 0, p.step[0]);
+    y_in.ask(a.dy, to + In::kTurn, me, bytes, to_ask > 0, p.step[1]);
+    if (kResidual) r_in.ask(a.residual, to + 2 * In::kTurn, me, bytes, to_ask > 0, p.step[2]);
+    to_ask -= apart;
+    copy_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth - 1; ++k) ask(slot0 + k * kStage);
+  grid_dep_launch();
+  const float inv = 1.0f / (float)a.width;
+  const long long w_at = set * a.weight_gstride;
+  auto weights = [&](int c, L (&f)[N]) {
+    load_param<T, V>(a.weight, a.param_dtype, a.param_vec, w_at, me.column(c), a.width, kRms ? 0.0f : 1.0f,
+                     kRms ? 1.0f : 0.0f, f);
+  };
+  L w[kHold ? C : 1][N], aw[C][N], ab[C][N];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if constexpr (kHold) weights(c, w[c]);
+#pragma unroll
+    for (int e = 0; e < N; ++e) aw[c][e] = ab[c][e] = v_of<L>(0.0f);
+  }
+  uint8_t* out = static_cast<uint8_t*>(a.dx) + (row * a.dx_stride + me.first) * (long long)sizeof(T);
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  if (!kRms && me.sub < left) {
+    next_mean = __ldg(a.mean + row);
+    next_rstd = __ldg(a.rstd + row);
+  }
+  const uint32_t last = slot0 + (kDepth - 1) * kStage;
+  uint32_t stage = slot0, ahead = last;
+  for (int turn = 0; left > 0; turn ^= 1) {
+    if (V < 4) __syncwarp();  // (the warp has read what now makes room)
+    ask(ahead);
+    float mean = next_mean, rstd = next_rstd;
+    if (!kRms && me.sub < left - apart) {
+      next_mean = __ldg(a.mean + row + apart);
+      next_rstd = __ldg(a.rstd + row + apart);
+    }
+    copy_wait<kDepth - 1>();
+    if (V < 4) __syncwarp();
+    const bool mine = me.sub < left;
+    const L m = v_of<L>(-mean);
+    L x[kHold ? C : 1][N], y[kHold ? C : 1][N];  // x: less its mean
+    L t1 = v_of<L>(0.0f), t2 = v_of<L>(0.0f);
+    auto load = [&](int c, L (&xc)[N], L (&yc)[N]) {
+      x_in.load(stage, me, c, p.step[0], xc);
+      y_in.load(stage + In::kTurn, me, c, p.step[1], yc);
+    };
+    auto add = [&](L (&xc)[N], const L (&yc)[N], const L (&wc)[N]) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const L g = v_mul(yc[e], wc[e]);
+        if (kRms) {
+          t1 = v_fma(xc[e], xc[e], t1);
+        } else {
+          xc[e] = v_add(xc[e], m);
+          t1 = v_add(g, t1);
+        }
+        t2 = v_fma(g, xc[e], t2);
+      }
+    };
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if constexpr (kHold) {
+        load(c, x[c], y[c]);
+        add(x[c], y[c], w[c]);
+      } else {
+        L xc[N], yc[N], wc[N];
+        load(c, xc, yc);
+        weights(c, wc);
+        add(xc, yc, wc);
+      }
+    }
+    float s1 = v_sum(t1), s2 = v_sum(t2);
+    if (wide) {
+      // both sums in one butterfly: the lower half of the warp goes on with s1, the upper with s2
+      const bool upper = lane >= 16;
+      float keep = upper ? s2 : s1;
+      keep += __shfl_xor_sync(0xffffffffu, upper ? s1 : s2, 16);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+      if ((lane & 15) == 0) reinterpret_cast<float*>(&parts[turn][warp])[lane >> 4] = keep;
+      group_sync(me.group, p.row_warps);
+      const float2 part = parts[turn][me.group * p.row_warps + (lane & 15)];
+      const float2 both = warps_sum2((lane & 15) < p.row_warps ? (upper ? part.y : part.x) : 0.0f);
+      s1 = both.x;
+      s2 = both.y;
+    } else {
+      s1 = lanes_sum(s1, p.row_lanes);
+      s2 = lanes_sum(s2, p.row_lanes);
+    }
+    if (kRms) rstd = rsqrtf(fmaf(s1, inv, a.eps));
+    float c1 = kRms ? 0.0f : s1 * inv, c2 = s2 * rstd * inv;
+    bool gone = !(fabsf((c1 + c2) + (rstd + mean)) <= kMax);
+    if (wide ? gone : __any_sync(0xffffffffu, gone)) {  // does the row have a gradient at all?
+      bool any = false;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        L xc[N], yc[N];
+        load(c, xc, yc);
+#pragma unroll
+        for (int e = 0; e < N; ++e) any |= v_any(yc[e]);
+      }
+      if (wide) {
+        gone = !group_any(any, me.group, p.row_warps);
+      } else {
+        const uint32_t lanes = __ballot_sync(0xffffffffu, any) >> (me.sub * p.row_lanes);
+        gone = gone && (p.row_lanes == 32 ? lanes : lanes & ((1u << p.row_lanes) - 1u)) == 0;
+      }
+      if (gone) {
+        rstd = c1 = c2 = 0.0f;
+        if constexpr (kHold) {
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[c][e] = v_of<L>(0.0f);
+        }
+      }
+    } else {
+      gone = false;
+    }
+    const L rs = v_of<L>(rstd), nc1 = v_of<L>(-c1), nc2 = v_of<L>(-c2);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      L xc[N], yc[N], wc[N], o[N];
+      if constexpr (kHold) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          xc[e] = x[c][e];
+          yc[e] = y[c][e];
+          wc[e] = w[c][e];
+        }
+      } else {
+        load(c, xc, yc);
+        weights(c, wc);
+#pragma unroll
+        for (int e = 0; e < N; ++e) xc[e] = gone ? v_of<L>(0.0f) : kRms ? xc[e] : v_add(xc[e], m);
+      }
+      if constexpr (kResidual) {
+        r_in.load(stage + 2 * In::kTurn, me, c, p.step[2], o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] = v_of<L>(0.0f);
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const L xn = v_mul(xc[e], rs);
+        aw[c][e] = v_fma(yc[e], xn, aw[c][e]);
+        ab[c][e] = v_add(yc[e], ab[c][e]);
+        const L g = kRms ? v_mul(yc[e], wc[e]) : v_fma(yc[e], wc[e], nc1);
+        const L t = v_fma(xn, nc2, g);
+        o[e] = kResidual ? v_fma(t, rs, o[e]) : v_mul(t, rs);
+      }
+      if (bytes[c] != 0 && mine) P::store(out + c * me.apart * (int)sizeof(T), bytes[c], o);
+    }
+    left -= apart;
+    row += apart;
+    out += p.step[3];
+    stage = stage == last ? slot0 : stage + kStage;
+    ahead = ahead == last ? slot0 : ahead + kStage;
+  }
+  copy_wait<0>();
+  if (a.dweight == nullptr && a.dbias == nullptr) return;
+  // The groups' sums, in place of the copies: [group][2][width].
+  __syncthreads();
+  if (p.batch > 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+#pragma unroll
+        for (int o = 16; o >= 4; o >>= 1)
+          if (o >= p.row_lanes) {
+            aw[c][e] = v_add(aw[c][e], __shfl_xor_sync(0xffffffffu, aw[c][e], o));
+            ab[c][e] = v_add(ab[c][e], __shfl_xor_sync(0xffffffffu, ab[c][e], o));
+          }
+  }
+  float* sums = reinterpret_cast<float*>(memory);
+  if (me.group < p.groups && me.sub == 0) {
+    float* to = sums + (size_t)me.group * 2 * a.width;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = me.column(c);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if constexpr (V == 1) {
+          if (col < a.width) {
+            to[col] = aw[c][e];
+            to[a.width + col] = ab[c][e];
+          }
+        } else {
+          const int at = col + 2 * e;
+          float lo, hi;
+          f2_unpack(aw[c][e], lo, hi);
+          if (at < a.width) to[at] = lo;
+          if (at + 1 < a.width) to[at + 1] = hi;
+          f2_unpack(ab[c][e], lo, hi);
+          if (at < a.width) to[a.width + at] = lo;
+          if (at + 1 < a.width) to[a.width + at + 1] = hi;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  float* to = p.cluster > 0 ? sums : a.partial + (long long)blockIdx.x * 2 * a.width;  // (in a cluster: the first group's place)
+  for (int c = threadIdx.x; c < 2 * a.width; c += kThreads) {
+    float t = 0.0f;
+    for (int g = 0; g < p.groups; ++g) t += sums[(size_t)g * 2 * a.width + c];
+    to[c] = t;
+  }
+  if (p.cluster == 0) return;
+  // The cluster is all CTAs of the set: each adds up its share of the columns.
+  cluster_sync();
+  const int rank = (int)cluster_rank();
+  const bool both = a.dweight == a.dbias;
+  const long long at = set * a.sum_gstride;
+  for (int c = rank * kThreads + threadIdx.x; c < a.width; c += p.cluster * kThreads) {
+    float dw = 0.0f, db = 0.0f;
+    for (int r = 0; r < p.cluster; ++r) {
+      float v, u;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(sums + c, (uint32_t)r)) : "memory");
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(cluster_addr(sums + a.width + c, (uint32_t)r)) : "memory");
+      dw += v;
+      db += u;
+    }
+    if (both) {
+      a.dweight[at + c] = dw + db;
+    } else {
+      if (a.dweight != nullptr) a.dweight[at + c] = dw;
+      if (a.dbias != nullptr) a.dbias[at + c] = db;
+    }
+  }
+  cluster_sync();  // nobody leaves while its sums are being read
+}
+
+// dweight and dbias: the sums of the CTAs' parts [set][part][2][width].  A CTA takes 32 of the 2 width columns, its 8 warps
+// every 8th part each, and adds the warps up in order.  both: the two go to one row, added.
+__global__ void __launch_bounds__(256) norm_sum_kernel(const float* __restrict__ partial, int parts, int width, float* dweight,
+                                                       float* dbias, long long sum_gstride, int blocks) {
+  __shared__ float sums[8][33];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int set = blockIdx.x / blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = (blockIdx.x - set * blocks) * 32 + lane;
+  const bool both = dweight == dbias;
+  float t = 0.0f;
+  if (c < (both ? width : 2 * width)) {
+    const float* p = partial + (long long)set * parts * 2 * width + c;
+#pragma unroll 4
+    for (int i = warp; i < parts; i += 8) {
+      t += p[(long long)i * 2 * width];
+      if (both) t += p[(long long)i * 2 * width + width];
+    }
+  }
+  sums[warp][lane] = t;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) t += sums[i][lane];
+  const long long at = set * sum_gstride;
+  if (c < width) {
+    if (dweight != nullptr) dweight[at + c] = t;
+  } else if (c < 2 * width && dbias != nullptr && !both) {
+    dbias[at + c - width] = t;
+  }
+}
+
+int norm_bwd_parts(int groups, int seq, int num_sms) {
+  const int most = num_sms / groups > 0 ? num_sms / groups : 1;
+  return seq < most ? seq : most;
+}
+
+template <typename T, int V, int E, int kWarps, bool kRms, bool kResidual>
+cudaError_t norm_bwd_launch_kernel(const NormBwdArgs& a, const Plan& p, int parts, bool sums, cudaStream_t s) {
+  constexpr int kInputs = kResidual ? 3 : 2, kTurn = Reader<T, V, E / V, 1, kWarps>::kTurn, kDepth = depth_of(kInputs, kTurn);
+  constexpr auto kKernel = norm_bwd_kernel<T, V, E, kDepth, kWarps, kRms, kResidual>;
+  const size_t copies = (size_t)kDepth * kInputs * kTurn, rows = sums ? (size_t)p.groups * 2 * a.width * sizeof(float) : 0;
+  const size_t memory = copies > rows ? copies : rows;
+  cudaError_t e = allow_ring<kKernel>();
+  if (e != cudaSuccess) return e;
+  const dim3 grid(parts * a.groups), block(kWarps * 32);
+  if (p.cluster > 0) return launch_kernel_cluster(kKernel, grid, block, memory, (unsigned)p.cluster, s, a, p, parts);
+  return launch_kernel(kKernel, grid, block, memory, s, true, a, p, parts);
+}
+
+template <typename T, int V, int E, int kWarps, bool kRms>
+cudaError_t norm_bwd_run(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
+  int parts = norm_bwd_parts(a.groups, a.seq, num_sms);
+  const bool sums = a.dweight != nullptr || a.dbias != nullptr;
+  bool second = sums;
+  if (parts > 0) {
+    Plan p = make_plan(a.width, V, E, kWarps);
+    const long long strides[4] = {a.x_stride, a.dy_stride, a.residual_stride, a.dx_stride};
+    for (int i = 0; i < 4; ++i) p.step[i] = p.apart * strides[i] * (long long)sizeof(T);
+    const int need = (a.seq - 1) / p.apart + 1;
+    parts = need < parts ? need : parts;
+    if (sums && need <= kCluster * kClusterTurns && a.groups * kCluster <= num_sms) {
+      p.cluster = 1;
+      while (p.cluster < kCluster && p.cluster < need) p.cluster *= 2;  // (a CTA may be left without rows)
+      parts = p.cluster;
+      second = false;
+    }
+    cudaError_t e = a.residual != nullptr ? norm_bwd_launch_kernel<T, V, E, kWarps, kRms, true>(a, p, parts, sums, s)
+                                          : norm_bwd_launch_kernel<T, V, E, kWarps, kRms, false>(a, p, parts, sums, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (!second) return cudaSuccess;
+  const int blocks = ((a.dweight == a.dbias ? 1 : 2) * a.width + 31) / 32;
+  return launch_kernel(norm_sum_kernel, dim3(blocks * a.groups), dim3(256), 0, s, true, (const float*)a.partial, parts, a.width,
+                       a.dweight, a.dbias, a.sum_gstride, blocks);
+}
+
+// Columns of a lane: the fewer registers a row takes, the more warps there can be.  rms: 8 with 24 warps (40 M elements with a
+// residual: 59 us at width 3072, 60 at 2560; with 16 and 16 warps 67, 66).  Layer norm: 16 (61 us at 2560, 62 at 4096; with 8
+// 65, 71), in odd rows 8 (20 M, no residual: 70 us at width 1023; with 16 82).  32 where these do not hold a row.
+template <typename T, int V, bool kRms>
+cudaError_t norm_bwd_any(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
+  if constexpr (kRms) {
+    return norm_bwd_run<T, V, 8, 24, true>(a, num_sms, s);  // (at most 4096 columns: 16 warps)
+  } else {
+    if (a.width > 16 * 32 * 16) return norm_bwd_run<T, V, 32, 16, false>(a, num_sms, s);
+    if constexpr (V < 4)
+      if (a.width <= 16 * 32 * 8) return norm_bwd_run<T, V, 8, 16, false>(a, num_sms, s);
+    return norm_bwd_run<T, V, 16, 16, false>(a, num_sms, s);
+  }
+}
+
+template <typename T, int V>
+cudaError_t norm_bwd_type(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
+  const long long size = sizeof(T);
+  if (a.width % V == 0 && on16(a.x, a.x_stride * size) && on16(a.dy, a.dy_stride * size) && on16(a.dx, a.dx_stride * size) &&
+      on16(a.residual, a.residual_stride * size))
+    return norm_bwd_any<T, V, false>(a, num_sms, s);
+  return norm_bwd_any<T, sizeof(T) == 4 ? 1 : 2, false>(a, num_sms, s);
+}
+
+}  // namespace
+
+size_t norm_bwd_workspace(int groups, int seq, int width, int num_sms) {
+  return (size_t)groups * norm_bwd_parts(groups, seq, num_sms) * 2 * width * sizeof(float);
+}
+
+cudaError_t norm_bwd_launch(const NormBwdArgs& given, int num_sms, cudaStream_t s) {
+  NormBwdArgs a = given;
+  a.param_vec = on16(a.weight, a.weight_gstride * (a.param_dtype == MI_F32 ? 4 : 2));
+  if (a.rms) return norm_bwd_any<__nv_bfloat16, 8, true>(a, num_sms, s);
+  if (a.dtype == MI_F32) return norm_bwd_type<float, 4>(a, num_sms, s);
+  if (a.dtype == MI_F16) return norm_bwd_type<__half, 8>(a, num_sms, s);
+  return norm_bwd_type<__nv_bfloat16, 8>(a, num_sms, s);
+}
+
+}  // namespace mi

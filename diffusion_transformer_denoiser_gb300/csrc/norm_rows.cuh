@@ -1,0 +1,388 @@
+// What the kernels of layer norm, its gradient and the modulated RMSNorm's gradient (layer_norm.cu, norm_bwd.cu) share.
+//
+// All three need sums over a row before they can write it, and are bound by HBM (forward 2 values an element, backward 3, or
+// 4 with a residual gradient).  They share one scheme.  A CTA per SM takes a contiguous part of the rows.  Groups of warps
+// share a row (or a warp takes several short rows), a lane with the same E columns of every row, whose weights and, backward,
+// sums over rows stay in its registers.  Rows are copied asynchronously into shared memory some turns ahead, so the reads
+// stream whatever the sums wait for.  No warp waits for another warp's copies; a group meets once a row, for the sums.
+//
+// Where every tensor's rows are on 16-byte boundaries, a lane copies and moves vectors of V elements = 16 bytes.  Rows that
+// begin anywhere are copied by the 16-byte granules that hold a warp's columns, and read word by word: single columns of fp32
+// (V = 1), pairs of 16-bit columns (V = 2, put together from two words where the row begins in the middle of one).
+//
+// Sums are fp32 in a fixed order: a lane's columns, a butterfly over the warp, the row's warps; over rows a lane's
+// rows, the CTA's lanes of the same columns, the CTAs.  Results repeat bit for bit.
+//
+// Measured on the way (GB300, bf16; 8260 x 2560 backward with a residual / 16418 x 4096 forward, us): one row a CTA at a
+// time from L1 368 / 141; rows by bulk copies of one thread a group into a ring with barriers 51 / 64 (the one thread's copies,
+// and every branch, are on the row's chain of about 1400 cycles); sums and outputs as two phases over tiles of rows, each
+// with its own mapping of threads, 56 / 67 (twice the instructions); a lane's own copies 39 / 51.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "../../include/mi_block.h"
+#include "mi_internal.h"
+#include "ptx.cuh"
+
+namespace mi {
+
+namespace {
+
+constexpr int kRingBytes = 200 * 1024;   // of the 227 KB of shared memory that a CTA may have
+
+// ------------------------------------------------------------------------------- element types
+// One or two values in fp32: the kernels' arithmetic is written once for both.
+__device__ __forceinline__ float v_add(float a, float b) { return a + b; }
+__device__ __forceinline__ float v_mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float v_fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float v_sum(float a) { return a; }
+__device__ __forceinline__ f32x2_t v_add(f32x2_t a, f32x2_t b) { return f2_add(a, b); }
+__device__ __forceinline__ f32x2_t v_mul(f32x2_t a, f32x2_t b) { return f2_mul(a, b); }
+__device__ __forceinline__ f32x2_t v_fma(f32x2_t a, f32x2_t b, f32x2_t c) { return f2_fma(a, b, c); }
+__device__ __forceinline__ float v_sum(f32x2_t a) {
+  float lo, hi;
+  f2_unpack(a, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ bool v_any(float a) { return a != 0.0f; }
+__device__ __forceinline__ bool v_any(f32x2_t a) { return (a & 0x7fffffff7fffffffull) != 0; }
+template <typename L> __device__ __forceinline__ L v_of(float a);
+template <> __device__ __forceinline__ float v_of<float>(float a) { return a; }
+template <> __device__ __forceinline__ f32x2_t v_of<f32x2_t>(float a) { return f2_of(a); }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Two 16-bit values in a word as fp32, and back (rounded once).
+template <typename T> __device__ __forceinline__ f32x2_t unpack2(uint32_t w) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return f2_pack(t.x, t.y);
+  } else {
+    return f2_pack(bf16_lo(w), bf16_hi(w));
+  }
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(f32x2_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return pack_bf16x2(lo, hi);
+  }
+}
+
+// Copies `bytes` of 16 and fills up with zeros (0: nothing is read).
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
+__device__ __forceinline__ uint4 load_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// V columns of a row: N numbers of type L in fp32.
+//   load   gives them from shared memory (words: `src` is the row's address in global memory, mod 2^32)
+//   store  writes them to `dst`, where `bytes` (not 0) of them are in the row
+template <typename T, int V> struct Piece;
+template <> struct Piece<float, 1> {
+  using L = float;
+  static constexpr int N = 1;
+  __device__ __forceinline__ static void load(uint32_t at, uint32_t, L (&f)[1]) {
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(at) : "memory");
+  }
+  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t, const L (&f)[1]) { *reinterpret_cast<float*>(dst) = f[0]; }
+};
+template <> struct Piece<float, 4> {
+  using L = f32x2_t;
+  static constexpr int N = 2;
+  __device__ __forceinline__ static void load(uint32_t at, L (&f)[2]) {
+    const uint4 v = load_shared16(at);
+    f[0] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t, const L (&f)[2]) {
+    float4 v;
+    f2_unpack(f[0], v.x, v.y);
+    f2_unpack(f[1], v.z, v.w);
+    *reinterpret_cast<float4*>(dst) = v;
+  }
+};
+template <typename T> struct Piece<T, 8> {
+  using L = f32x2_t;
+  static constexpr int N = 4;
+  __device__ __forceinline__ static void load(uint32_t at, L (&f)[4]) {
+    const uint4 v = load_shared16(at);
+    f[0] = unpack2<T>(v.x);
+    f[1] = unpack2<T>(v.y);
+    f[2] = unpack2<T>(v.z);
+    f[3] = unpack2<T>(v.w);
+  }
+  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t, const L (&f)[4]) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<T>(f[0]), pack2<T>(f[1]), pack2<T>(f[2]), pack2<T>(f[3]));
+  }
+};
+template <typename T> struct Piece<T, 2> {
+  using L = f32x2_t;
+  static constexpr int N = 1;
+  __device__ __forceinline__ static void load(uint32_t at, uint32_t src, L (&f)[1]) {
+    uint32_t lo, hi;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo) : "r"(at) : "memory");
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(hi) : "r"(at + 4) : "memory");
+    f[0] = unpack2<T>(__funnelshift_r(lo, hi, (src & 2u) * 8));
+  }
+  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t bytes, const L (&f)[1]) {
+    const uint32_t w = pack2<T>(f[0]);
+    if ((reinterpret_cast<uintptr_t>(dst) & 2u) == 0 && bytes == 4) {
+      *reinterpret_cast<uint32_t*>(dst) = w;
+    } else {
+      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w;
+      if (bytes == 4) *reinterpret_cast<uint16_t*>(dst + 2) = (uint16_t)(w >> 16);
+    }
+  }
+};
+
+template <typename L> __device__ __forceinline__ L v_of2(float a, float b) {
+  if constexpr (sizeof(L) == 8) return f2_pack(a, b);
+  else return a;
+}
+
+// Entry i of a parameter of the given type; p null: `none`.
+__device__ __forceinline__ float param_at(const void* p, int dtype, long long i, float none) {
+  if (p == nullptr) return none;
+  if (dtype == MI_F32) return static_cast<const float*>(p)[i];
+  if (dtype == MI_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// A lane's V columns from col on of a parameter, `plus` added (zeros past the width).  T: the rows' type, which the
+// parameter has unless it is fp32; aligned: the parameter is on a 16-byte boundary.
+template <typename T, int V>
+__device__ __forceinline__ void load_param(const void* p, int dtype, bool aligned, long long at, int col, int width, float none,
+                                           float plus, typename Piece<T, V>::L (&w)[Piece<T, V>::N]) {
+  using P = Piece<T, V>;
+  using L = typename P::L;
+  if constexpr (V >= 4) if (p != nullptr && aligned && col < width) {
+    if (sizeof(T) == 4 || dtype == MI_F32) {
+      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + col);
+#pragma unroll
+      for (int i = 0; i < P::N; i += 2) {
+        const float4 v = f[i / 2];
+        w[i] = v_of2<L>(v.x, v.y);
+        w[i + 1] = v_of2<L>(v.z, v.w);
+      }
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p) + at + col);
+      const uint32_t f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < P::N; ++i) w[i] = unpack2<T>(f[i % 4]);
+    }
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) w[i] = v_add(w[i], v_of<L>(plus));
+    return;
+  }
+  float f[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) f[e] = col + e < width ? param_at(p, dtype, at + col + e, none) + plus : 0.0f;
+#pragma unroll
+  for (int i = 0; i < P::N; ++i) w[i] = V == 1 ? v_of<L>(f[0]) : v_of2<L>(f[(2 * i) % V], f[(2 * i + 1) % V]);
+}
+
+// ---------------------------------------------------------------------------------------------- rows
+// How a launch spreads rows over lanes.
+struct Plan {
+  int row_warps;               // warps that share a row
+  int row_lanes;               // lanes of a row in a warp: 32, or fewer (a power of two) with several rows a warp
+  int batch;                   // rows that a group takes at a time: 32 / row_lanes
+  int groups;                  // of a CTA
+  int apart;                   // rows between a group's batches
+  int cluster;                 // CTAs of a cluster that sum rows up together (backward; 0: a second kernel does)
+  long long step[4];           // and bytes: of x, dy, the residual; of the output
+};
+
+// This thread's place: which rows of the CTA it takes, and which columns: piece c is columns [first + c apart, + V).
+template <int V, int C>
+struct Place {
+  int group, row_warp, sub, lane, row_lanes, first, apart;  // lane: of the row in this warp
+  __device__ __forceinline__ explicit Place(const Plan& p) {
+    const int warp = threadIdx.x >> 5;
+    group = warp / p.row_warps;
+    row_warp = warp - group * p.row_warps;
+    row_lanes = p.row_lanes;
+    sub = (threadIdx.x & 31) / p.row_lanes;
+    lane = (threadIdx.x & 31) - sub * p.row_lanes;
+    first = (row_warp * C * 32 + lane) * V;
+    apart = p.row_lanes * V;
+  }
+  __device__ __forceinline__ int column(int c) const { return first + c * apart; }
+};
+
+// One input's rows, as a thread reads them: it asks for its part of rows kDepth - 1 turns before it loads them.  Columns and
+// rows that are not there read as zeros.
+template <typename T, int V, int C, int kDepth, int kWarps, bool kVectors = (V >= 4)>
+struct Reader;
+
+// Vectors: a lane copies its own pieces.
+template <typename T, int V, int C, int kDepth, int kWarps>
+struct Reader<T, V, C, kDepth, kWarps, true> {
+  using P = Piece<T, V>;
+  static constexpr int kTurn = C * kWarps * 32 * 16;  // shared memory of an input's turn
+  const uint8_t* next;  // this thread's first piece in the row to be asked for next
+
+  __device__ __forceinline__ Reader(const void* tensor, long long stride, long long row, int, const Place<V, C>& me)
+      : next(static_cast<const uint8_t*>(tensor) + (row * stride + me.first) * (long long)sizeof(T)) {}
+  __device__ __forceinline__ static uint32_t place(uint32_t memory, const Place<V, C>&) { return memory + threadIdx.x * 16; }
+  // to: the turn's shared memory, this thread's place in it.
+  __device__ __forceinline__ void ask(const void* tensor, uint32_t to, const Place<V, C>& me, const uint32_t (&bytes)[C], bool has,
+                                      long long step) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t n = has ? bytes[c] : 0u;
+      copy_async(to + c * kWarps * 32 * 16, n != 0 ? next + c * me.apart * (int)sizeof(T) : static_cast<const uint8_t*>(tensor), n);
+    }
+    next += step;
+  }
+  __device__ __forceinline__ void load(uint32_t from, const Place<V, C>&, int c, long long, typename P::L (&f)[P::N]) const {
+    P::load(from + c * kWarps * 32 * 16, f);
+  }
+};
+
+// Words: the lanes of a row copy the granules of their C row_lanes columns or pairs of columns (and one more: they may begin in
+// the middle of a granule); a lane reads other lanes' copies, so a warp meets (__syncwarp) between copies and reads.
+template <typename T, int V, int C, int kDepth, int kWarps>
+struct Reader<T, V, C, kDepth, kWarps, false> {
+  using P = Piece<T, V>;
+  static constexpr int kWarp = (8 * C + 8) * 16;  // a warp's: C / 4 granules a lane, and one more for each of up to 8 rows
+  static constexpr int kTurn = kWarps * kWarp;
+  const uint8_t* next;  // the warp's first column in the row to be asked for next
+  int left;             // bytes of the row from there on
+
+  __device__ __forceinline__ Reader(const void* tensor, long long stride, long long row, int width, const Place<V, C>& me) {
+    const int first = me.row_warp * C * 32 * V;
+    next = static_cast<const uint8_t*>(tensor) + (row * stride + first) * (long long)sizeof(T);
+    left = max(width - first, 0) * (int)sizeof(T);
+  }
+  __device__ __forceinline__ static uint32_t place(uint32_t memory, const Place<V, C>& me) {
+    return memory + (threadIdx.x >> 5) * kWarp + me.sub * (me.row_lanes * (C / 4) + 1) * 16;
+  }
+  __device__ __forceinline__ void granule(const void* tensor, uint32_t to, const uint8_t* start, int lead, int g, int n) const {
+    const int size = min(max(n + lead - 16 * g, 0), 16);
+    const uint8_t* src = start + 16 * g;
+    if (size > 0 && src < tensor) {  // (the tensor's first row: a granule that begins in front of it)
+#pragma unroll 1
+      for (int i = 0; i < 16; i += (int)sizeof(T)) {
+        const bool in = src + i >= tensor && i < size;
+        if constexpr (sizeof(T) == 4) {
+          const uint32_t v = in ? *reinterpret_cast<const uint32_t*>(src + i) : 0u;
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 16 * g + i), "r"(v) : "memory");
+        } else {
+          const uint16_t v = in ? *reinterpret_cast<const uint16_t*>(src + i) : (uint16_t)0;
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 16 * g + i), "h"(v) : "memory");
+        }
+      }
+    } else {
+      copy_async(to + 16 * g, size > 0 ? src : start, (uint32_t)size);
+    }
+  }
+  __device__ __forceinline__ void ask(const void* tensor, uint32_t to, const Place<V, C>& me, const uint32_t (&)[C], bool has,
+                                      long long step) {
+    const int lead = (int)(reinterpret_cast<uintptr_t>(next) & 15u), n = has ? left : -16;
+    const uint8_t* start = next - lead;
+#pragma unroll
+    for (int k = 0; k < C / 4; ++k) granule(tensor, to, start, lead, k * me.row_lanes + me.lane, n);
+    if (me.lane == 0) granule(tensor, to, start, lead, C / 4 * me.row_lanes, n);
+    next += step;
+  }
+  __device__ __forceinline__ void load(uint32_t from, const Place<V, C>& me, int c, long long step, typename P::L (&f)[P::N]) const {
+    const uint32_t src = (uint32_t)reinterpret_cast<uintptr_t>(next) - kDepth * (uint32_t)step;  // (where the row came from)
+    P::load(from + (src & 12u) + (c * me.row_lanes + me.lane) * 4, src, f);
+  }
+};
+
+__device__ __forceinline__ void group_sync(int group, int warps) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
+}
+
+// Whether any thread of the group has p.
+__device__ __forceinline__ bool group_any(bool p, int group, int warps) {
+  int r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"((int)p), "r"(group + 1), "r"(warps * 32) : "memory");
+  return r != 0;
+}
+
+// Sum over the `lanes` lanes of a row (without a branch: one costs as much as a shuffle here).
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v += o < lanes ? u : 0.0f;
+  }
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sums over the warps of a row, at most 16, of two values: lane i < 16 holds warp i's first one, lane 16 + i its second (zeros
+// where there is no warp).  All lanes get both.
+__device__ __forceinline__ float2 warps_sum2(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const float u = __shfl_xor_sync(0xffffffffu, v, 16);
+  return (threadIdx.x & 16) != 0 ? make_float2(u, v) : make_float2(v, u);
+}
+
+// ---------------------------------------------------------------------------------------------- host
+inline bool on16(const void* p, long long stride_bytes) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)stride_bytes) & 15u) == 0;
+}
+
+// A row of `width` over lanes of E columns in vectors of V.
+inline Plan make_plan(int width, int v, int e, int warps) {
+  Plan p = {};
+  const int threads = (width + e - 1) / e;  // of a row
+  p.row_warps = (threads + 31) / 32;
+  p.row_lanes = 32;
+  while (p.row_warps == 1 && p.row_lanes > 4 && p.row_lanes / 2 >= threads) p.row_lanes /= 2;
+  p.batch = 32 / p.row_lanes;
+  p.groups = warps / p.row_warps;
+  p.apart = p.groups * p.batch;
+  return p;
+}
+
+// Turns that the shared memory holds, up to 8.
+constexpr int depth_of(int inputs, int turn) {
+  const int fit = kRingBytes / (inputs * turn);
+  return fit < 8 ? fit : 8;
+}
+
+// Lets a kernel have that much shared memory, once a device.
+template <auto kKernel>
+cudaError_t allow_ring() {
+  static bool done[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
+}  // namespace
+
+}  // namespace mi
