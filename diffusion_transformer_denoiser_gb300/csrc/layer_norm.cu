@@ -9,18 +9,17 @@ namespace {
 // mean m and the squares q around it.  Over the warps of a row, A = sum n (m - m_0) and B = sum (q + n (m - m_0)^2) give the
 // row's mean m_0 + A / width and its squares B - A^2 / width.  (What that difference takes off is at most as many times what is
 // left as there are warps, 16: the row's squares are at least n_0 (m_0 - mean)^2, its first warp's.)
-template <typename T, int V, int E, int kDepth, int kWarps>
+template <typename T, int V, int E, int kDepth, int kWarps, bool kWide>
 __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerNormArgs a, const Plan p) {
   using P = Piece<T, V>;
   using L = typename P::L;
   constexpr int C = E / V, N = P::N, kThreads = kWarps * 32;
-  using In = Reader<T, V, C, kDepth, kWarps>;
+  using In = Reader<T, V, C, kWarps, kWide>;
   constexpr int kStage = In::kTurn;
   extern __shared__ __align__(128) uint8_t memory[];
   __shared__ float2 parts[2][kWarps + 16];  // a warp's mean and squares (read 16 from a group's first on)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place<V, C> me(p);
-  const bool wide = p.row_warps > 1;
+  const Place<V, C, kWide> me(p);
   grid_dep_wait();
   const long long row0 = (long long)a.rows * blockIdx.x / gridDim.x;
   const int rows = (int)((long long)a.rows * (blockIdx.x + 1) / gridDim.x - row0);
@@ -34,7 +33,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
   const uint32_t slot0 = In::place(smem_u32(memory), me);
   int to_ask = left - me.sub;  // rows of this thread
   auto ask = [&](uint32_t to) {
-    x_in.ask(a.x, to, me, bytes, to_ask > 0, p.step[0]);
+    x_in.ask(a.x, to, me, bytes, to_ask > 0, to_ask > apart, p.step[0]);
     to_ask -= apart;
     copy_commit();
   };
@@ -48,7 +47,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
     for (int c = 0; c < C; ++c) n += min(max(a.width - (w * C + c) * 32 * V, 0), 32 * V);
     return (float)n;
   };
-  const float inv_cols = wide ? 1.0f / fmaxf(columns_of(me.row_warp), 1.0f) : inv;
+  const float inv_cols = kWide ? 1.0f / fmaxf(columns_of(me.row_warp), 1.0f) : inv;
   const float n_of_lane = (lane & 15) < p.row_warps ? columns_of(lane & 15) : 0.0f;
   L w[C][N], b[C][N];
 #pragma unroll
@@ -68,11 +67,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
     L t = v_of<L>(0.0f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      x_in.load(stage, me, c, p.step[0], x[c]);
+      x_in.load(stage, me, c, x[c]);
 #pragma unroll
       for (int e = 0; e < N; ++e) t = v_add(t, x[c][e]);
     }
-    const float s = wide ? warp_sum(v_sum(t)) : lanes_sum(v_sum(t), p.row_lanes);
+    const float s = kWide ? warp_sum(v_sum(t)) : lanes_sum(v_sum(t), p.row_lanes);
     const float m = s * inv_cols;
     t = v_of<L>(0.0f);
 #pragma unroll
@@ -84,8 +83,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
         t = v_fma(d, d, t);
       }
     }
-    float mean = m, square = wide ? warp_sum(v_sum(t)) : lanes_sum(v_sum(t), p.row_lanes);
-    if (wide) {
+    float mean = m, square = kWide ? warp_sum(v_sum(t)) : lanes_sum(v_sum(t), p.row_lanes);
+    if constexpr (kWide) {
       if (lane == 0) parts[turn][warp] = make_float2(m, square);
       group_sync(me.group, p.row_warps);
       const float first = parts[turn][me.group * p.row_warps].x;
@@ -104,12 +103,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
       L o[N];
 #pragma unroll
       for (int e = 0; e < N; ++e) o[e] = v_fma(v_mul(v_add(x[c][e], nm), rs), w[c][e], b[c][e]);
-      if (bytes[c] != 0 && mine) P::store(out + c * me.apart * (int)sizeof(T), bytes[c], o);
+      P::store(out + c * me.apart() * (int)sizeof(T), mine ? bytes[c] : 0u, o);
     }
     if (me.first == 0 && mine) {
       if (a.mean != nullptr) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
+    x_in.advance(p.step[0]);
     left -= apart;
     row += apart;
     out += p.step[3];
@@ -119,18 +119,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
   copy_wait<0>();
 }
 
+template <typename T, int V, int E, int kWarps, bool kWide>
+cudaError_t layer_norm_start(const LayerNormArgs& a, const Plan& p, int grid, cudaStream_t s) {
+  constexpr int kTurn = Reader<T, V, E / V, kWarps, kWide>::kTurn, kDepth = depth_of(1, kTurn);
+  constexpr auto kKernel = layer_norm_kernel<T, V, E, kDepth, kWarps, kWide>;
+  cudaError_t e = allow_ring<kKernel>();
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kKernel, dim3(grid), dim3(kWarps * 32), (size_t)kDepth * kTurn, s, true, a, p);
+}
+
 template <typename T, int V, int E, int kWarps>
 cudaError_t layer_norm_run(const LayerNormArgs& a, int num_sms, cudaStream_t s) {
-  constexpr int kTurn = Reader<T, V, E / V, 1, kWarps>::kTurn, kDepth = depth_of(1, kTurn);
-  constexpr auto kKernel = layer_norm_kernel<T, V, E, kDepth, kWarps>;
-  Plan p = make_plan(a.width, V, E, kWarps);
+  Plan p = make_plan(a.width, E, kWarps);
   p.step[0] = p.apart * a.x_stride * (long long)sizeof(T);
   p.step[3] = p.apart * a.out_stride * (long long)sizeof(T);
   const long long need = ((long long)a.rows + p.apart - 1) / p.apart;
   const int grid = need < num_sms ? (int)need : num_sms;
-  cudaError_t e = allow_ring<kKernel>();
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kKernel, dim3(grid), dim3(kWarps * 32), (size_t)kDepth * kTurn, s, true, a, p);
+  if constexpr (E == 8 || (E == 16 && V >= 4))  // (wider pieces come with wide rows only)
+    if (p.row_warps == 1) return layer_norm_start<T, V, E, kWarps, false>(a, p, grid, s);
+  return layer_norm_start<T, V, E, kWarps, true>(a, p, grid, s);
 }
 
 // Columns of a lane: 16 (40 M bf16 elements: 31 us at width 256, 35 at 2560, 34 at 4096; with 8 and 24 warps 34, 43, 47), but 8

@@ -15,19 +15,18 @@ constexpr int kClusterTurns = 2;  // turns of their groups up to which that is d
 //   sums over rows: dweight += dy n, dbias += dy.
 // A row whose sums or statistics are not finite is looked at again: if its dy is zero it counts as absent (so what
 // padding holds reaches nothing), which costs rows that are finite nothing.
-template <typename T, int V, int E, int kDepth, int kWarps, bool kRms, bool kResidual>
+template <typename T, int V, int E, int kDepth, int kWarps, bool kWide, bool kRms, bool kResidual>
 __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdArgs a, const Plan p, int n_parts) {
   using P = Piece<T, V>;
   using L = typename P::L;
   constexpr int C = E / V, N = P::N, kInputs = kResidual ? 3 : 2, kThreads = kWarps * 32;
   constexpr bool kHold = E <= 16;  // a row in registers; wider rows are read from shared memory again, their weights from L1
-  using In = Reader<T, V, C, kDepth, kWarps>;
+  using In = Reader<T, V, C, kWarps, kWide>;
   constexpr int kStage = kInputs * In::kTurn;
   extern __shared__ __align__(128) uint8_t memory[];
   __shared__ float2 parts[2][kWarps + 16];  // a warp's sums (read 16 from a group's first on)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place<V, C> me(p);
-  const bool wide = p.row_warps > 1;
+  const Place<V, C, kWide> me(p);
   grid_dep_wait();
   const int set = blockIdx.x / n_parts, part_of_set = blockIdx.x - set * n_parts;
   const long long row0 = (long long)set * a.seq + (long long)a.seq * part_of_set / n_parts;
@@ -42,9 +41,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
   const uint32_t slot0 = In::place(smem_u32(memory), me);
   int to_ask = left - me.sub;
   auto ask = [&](uint32_t to) {
-    x_in.ask(a.x, to, me, bytes, to_ask > 0, p.step[0]);
-    y_in.ask(a.dy, to + In::kTurn, me, bytes, to_ask > 0, p.step[1]);
-    if (kResidual) r_in.ask(a.residual, to + 2 * In::kTurn, me, bytes, to_ask > 0, p.step[2]);
+    x_in.ask(a.x, to, me, bytes, to_ask > 0, to_ask > apart, p.step[0]);
+    y_in.ask(a.dy, to + In::kTurn, me, bytes, to_ask > 0, to_ask > apart, p.step[1]);
+    if (kResidual) r_in.ask(a.residual, to + 2 * In::kTurn, me, bytes, to_ask > 0, to_ask > apart, p.step[2]);
     to_ask -= apart;
     copy_commit();
   };
@@ -87,8 +86,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
     L x[kHold ? C : 1][N], y[kHold ? C : 1][N];  // x: less its mean
     L t1 = v_of<L>(0.0f), t2 = v_of<L>(0.0f);
     auto load = [&](int c, L (&xc)[N], L (&yc)[N]) {
-      x_in.load(stage, me, c, p.step[0], xc);
-      y_in.load(stage + In::kTurn, me, c, p.step[1], yc);
+      x_in.load(stage, me, c, xc);
+      y_in.load(stage + In::kTurn, me, c, yc);
     };
     auto add = [&](L (&xc)[N], const L (&yc)[N], const L (&wc)[N]) {
 #pragma unroll
@@ -116,7 +115,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
       }
     }
     float s1 = v_sum(t1), s2 = v_sum(t2);
-    if (wide) {
+    if constexpr (kWide) {
       // both sums in one butterfly: the lower half of the warp goes on with s1, the upper with s2
       const bool upper = lane >= 16;
       float keep = upper ? s2 : s1;
@@ -136,7 +135,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
     if (kRms) rstd = rsqrtf(fmaf(s1, inv, a.eps));
     float c1 = kRms ? 0.0f : s1 * inv, c2 = s2 * rstd * inv;
     bool gone = !(fabsf((c1 + c2) + (rstd + mean)) <= kMax);
-    if (wide ? gone : __any_sync(0xffffffffu, gone)) {  // does the row have a gradient at all?
+    if (kWide ? gone : (bool)__any_sync(0xffffffffu, gone)) {  // does the row have a gradient at all?
       bool any = false;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -145,7 +144,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
 #pragma unroll
         for (int e = 0; e < N; ++e) any |= v_any(yc[e]);
       }
-      if (wide) {
+      if constexpr (kWide) {
         gone = !group_any(any, me.group, p.row_warps);
       } else {
         const uint32_t lanes = __ballot_sync(0xffffffffu, any) >> (me.sub * p.row_lanes);
@@ -181,7 +180,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
         for (int e = 0; e < N; ++e) xc[e] = gone ? v_of<L>(0.0f) : kRms ? xc[e] : v_add(xc[e], m);
       }
       if constexpr (kResidual) {
-        r_in.load(stage + 2 * In::kTurn, me, c, p.step[2], o);
+        r_in.load(stage + 2 * In::kTurn, me, c, o);
       } else {
 #pragma unroll
         for (int e = 0; e < N; ++e) o[e] = v_of<L>(0.0f);
@@ -195,8 +194,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
         const L t = v_fma(xn, nc2, g);
         o[e] = kResidual ? v_fma(t, rs, o[e]) : v_mul(t, rs);
       }
-      if (bytes[c] != 0 && mine) P::store(out + c * me.apart * (int)sizeof(T), bytes[c], o);
+      P::store(out + c * me.apart() * (int)sizeof(T), mine ? bytes[c] : 0u, o);
     }
+    x_in.advance(p.step[0]);
+    y_in.advance(p.step[1]);
+    if (kResidual) r_in.advance(p.step[2]);
     left -= apart;
     row += apart;
     out += p.step[3];
@@ -314,10 +316,10 @@ int norm_bwd_parts(int groups, int seq, int num_sms) {
   return seq < most ? seq : most;
 }
 
-template <typename T, int V, int E, int kWarps, bool kRms, bool kResidual>
-cudaError_t norm_bwd_launch_kernel(const NormBwdArgs& a, const Plan& p, int parts, bool sums, cudaStream_t s) {
-  constexpr int kInputs = kResidual ? 3 : 2, kTurn = Reader<T, V, E / V, 1, kWarps>::kTurn, kDepth = depth_of(kInputs, kTurn);
-  constexpr auto kKernel = norm_bwd_kernel<T, V, E, kDepth, kWarps, kRms, kResidual>;
+template <typename T, int V, int E, int kWarps, bool kWide, bool kRms, bool kResidual>
+cudaError_t norm_bwd_start(const NormBwdArgs& a, const Plan& p, int parts, bool sums, cudaStream_t s) {
+  constexpr int kInputs = kResidual ? 3 : 2, kTurn = Reader<T, V, E / V, kWarps, kWide>::kTurn, kDepth = depth_of(kInputs, kTurn);
+  constexpr auto kKernel = norm_bwd_kernel<T, V, E, kDepth, kWarps, kWide, kRms, kResidual>;
   const size_t copies = (size_t)kDepth * kInputs * kTurn, rows = sums ? (size_t)p.groups * 2 * a.width * sizeof(float) : 0;
   const size_t memory = copies > rows ? copies : rows;
   cudaError_t e = allow_ring<kKernel>();
@@ -327,13 +329,20 @@ cudaError_t norm_bwd_launch_kernel(const NormBwdArgs& a, const Plan& p, int part
   return launch_kernel(kKernel, grid, block, memory, s, true, a, p, parts);
 }
 
+template <typename T, int V, int E, int kWarps, bool kRms, bool kResidual>
+cudaError_t norm_bwd_width(const NormBwdArgs& a, const Plan& p, int parts, bool sums, cudaStream_t s) {
+  if constexpr (E == 8 || (E == 16 && V >= 4))  // (wider pieces come with wide rows only)
+    if (p.row_warps == 1) return norm_bwd_start<T, V, E, kWarps, false, kRms, kResidual>(a, p, parts, sums, s);
+  return norm_bwd_start<T, V, E, kWarps, true, kRms, kResidual>(a, p, parts, sums, s);
+}
+
 template <typename T, int V, int E, int kWarps, bool kRms>
 cudaError_t norm_bwd_run(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
   int parts = norm_bwd_parts(a.groups, a.seq, num_sms);
   const bool sums = a.dweight != nullptr || a.dbias != nullptr;
   bool second = sums;
   if (parts > 0) {
-    Plan p = make_plan(a.width, V, E, kWarps);
+    Plan p = make_plan(a.width, E, kWarps);
     const long long strides[4] = {a.x_stride, a.dy_stride, a.residual_stride, a.dx_stride};
     for (int i = 0; i < 4; ++i) p.step[i] = p.apart * strides[i] * (long long)sizeof(T);
     const int need = (a.seq - 1) / p.apart + 1;
@@ -344,8 +353,8 @@ cudaError_t norm_bwd_run(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
       parts = p.cluster;
       second = false;
     }
-    cudaError_t e = a.residual != nullptr ? norm_bwd_launch_kernel<T, V, E, kWarps, kRms, true>(a, p, parts, sums, s)
-                                          : norm_bwd_launch_kernel<T, V, E, kWarps, kRms, false>(a, p, parts, sums, s);
+    const cudaError_t e = a.residual != nullptr ? norm_bwd_width<T, V, E, kWarps, kRms, true>(a, p, parts, sums, s)
+                                                : norm_bwd_width<T, V, E, kWarps, kRms, false>(a, p, parts, sums, s);
     if (e != cudaSuccess) return e;
   }
   if (!second) return cudaSuccess;

@@ -90,9 +90,15 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t at) {
   return v;
 }
 
+__device__ __forceinline__ void store_global16(uint8_t* at, uint32_t bytes, uint4 v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(at), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w), "r"(bytes)
+               : "memory");
+}
+
 // V columns of a row: N numbers of type L in fp32.
 //   load   gives them from shared memory (words: `src` is the row's address in global memory, mod 2^32)
-//   store  writes them to `dst`, where `bytes` (not 0) of them are in the row
+//   store  writes those of them to `dst` that are in the row, `bytes` (by predicates: a branch would cost more)
 template <typename T, int V> struct Piece;
 template <> struct Piece<float, 1> {
   using L = float;
@@ -100,7 +106,9 @@ template <> struct Piece<float, 1> {
   __device__ __forceinline__ static void load(uint32_t at, uint32_t, L (&f)[1]) {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(at) : "memory");
   }
-  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t, const L (&f)[1]) { *reinterpret_cast<float*>(dst) = f[0]; }
+  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t bytes, const L (&f)[1]) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.f32 [%0], %1;\n\t}" ::"l"(dst), "f"(f[0]), "r"(bytes) : "memory");
+  }
 };
 template <> struct Piece<float, 4> {
   using L = f32x2_t;
@@ -110,11 +118,11 @@ template <> struct Piece<float, 4> {
     f[0] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
     f[1] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t, const L (&f)[2]) {
+  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t bytes, const L (&f)[2]) {
     float4 v;
     f2_unpack(f[0], v.x, v.y);
     f2_unpack(f[1], v.z, v.w);
-    *reinterpret_cast<float4*>(dst) = v;
+    store_global16(dst, bytes, make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)));
   }
 };
 template <typename T> struct Piece<T, 8> {
@@ -127,8 +135,8 @@ template <typename T> struct Piece<T, 8> {
     f[2] = unpack2<T>(v.z);
     f[3] = unpack2<T>(v.w);
   }
-  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t, const L (&f)[4]) {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<T>(f[0]), pack2<T>(f[1]), pack2<T>(f[2]), pack2<T>(f[3]));
+  __device__ __forceinline__ static void store(uint8_t* dst, uint32_t bytes, const L (&f)[4]) {
+    store_global16(dst, bytes, make_uint4(pack2<T>(f[0]), pack2<T>(f[1]), pack2<T>(f[2]), pack2<T>(f[3])));
   }
 };
 template <typename T> struct Piece<T, 2> {
@@ -141,13 +149,13 @@ template <typename T> struct Piece<T, 2> {
     f[0] = unpack2<T>(__funnelshift_r(lo, hi, (src & 2u) * 8));
   }
   __device__ __forceinline__ static void store(uint8_t* dst, uint32_t bytes, const L (&f)[1]) {
-    const uint32_t w = pack2<T>(f[0]);
-    if ((reinterpret_cast<uintptr_t>(dst) & 2u) == 0 && bytes == 4) {
-      *reinterpret_cast<uint32_t*>(dst) = w;
-    } else {
-      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w;
-      if (bytes == 4) *reinterpret_cast<uint16_t*>(dst + 2) = (uint16_t)(w >> 16);
-    }
+    const uint32_t w = pack2<T>(f[0]), halves = ((uint32_t)reinterpret_cast<uintptr_t>(dst) & 2u) | (bytes ^ 4u);  // 0: the word at once
+    asm volatile(
+        "{\n\t.reg .pred word, lo, hi;\n\t.reg .b16 l, h;\n\tsetp.eq.u32 word, %2, 0;\n\tsetp.ne.u32 lo, %2, 0;\n\t"
+        "setp.eq.and.u32 hi, %3, 4, lo;\n\tsetp.ne.and.u32 lo, %3, 0, lo;\n\tmov.b32 {l, h}, %1;\n\t"
+        "@word st.global.b32 [%0], %1;\n\t@lo st.global.b16 [%0], l;\n\t@hi st.global.b16 [%0 + 2], h;\n\t}" ::"l"(dst),
+        "r"(w), "r"(halves), "r"(bytes)
+        : "memory");
   }
 };
 
@@ -210,102 +218,109 @@ struct Plan {
 };
 
 // This thread's place: which rows of the CTA it takes, and which columns: piece c is columns [first + c apart, + V).
-template <int V, int C>
+// kWide: warps share a row; otherwise rows share a warp, or have one each.
+template <int V, int C, bool kWide>
 struct Place {
-  int group, row_warp, sub, lane, row_lanes, first, apart;  // lane: of the row in this warp
+  int group, row_warp, sub, lane, first;  // lane: of the row in this warp
+  int lanes;
   __device__ __forceinline__ explicit Place(const Plan& p) {
     const int warp = threadIdx.x >> 5;
-    group = warp / p.row_warps;
-    row_warp = warp - group * p.row_warps;
-    row_lanes = p.row_lanes;
-    sub = (threadIdx.x & 31) / p.row_lanes;
-    lane = (threadIdx.x & 31) - sub * p.row_lanes;
+    lanes = p.row_lanes;
+    group = kWide ? warp / p.row_warps : warp;
+    row_warp = kWide ? warp - group * p.row_warps : 0;
+    sub = kWide ? 0 : (threadIdx.x & 31) / p.row_lanes;
+    lane = kWide ? threadIdx.x & 31 : (threadIdx.x & 31) - sub * p.row_lanes;
     first = (row_warp * C * 32 + lane) * V;
-    apart = p.row_lanes * V;
   }
-  __device__ __forceinline__ int column(int c) const { return first + c * apart; }
+  __device__ __forceinline__ int row_lanes() const { return kWide ? 32 : lanes; }
+  __device__ __forceinline__ int apart() const { return row_lanes() * V; }
+  __device__ __forceinline__ int column(int c) const { return first + c * apart(); }
 };
 
 // One input's rows, as a thread reads them: it asks for its part of rows kDepth - 1 turns before it loads them.  Columns and
 // rows that are not there read as zeros.
-template <typename T, int V, int C, int kDepth, int kWarps, bool kVectors = (V >= 4)>
+template <typename T, int V, int C, int kWarps, bool kWide, bool kVectors = (V >= 4)>
 struct Reader;
 
 // Vectors: a lane copies its own pieces.
-template <typename T, int V, int C, int kDepth, int kWarps>
-struct Reader<T, V, C, kDepth, kWarps, true> {
+template <typename T, int V, int C, int kWarps, bool kWide>
+struct Reader<T, V, C, kWarps, kWide, true> {
   using P = Piece<T, V>;
+  using At = Place<V, C, kWide>;
   static constexpr int kTurn = C * kWarps * 32 * 16;  // shared memory of an input's turn
   const uint8_t* next;  // this thread's first piece in the row to be asked for next
 
-  __device__ __forceinline__ Reader(const void* tensor, long long stride, long long row, int, const Place<V, C>& me)
+  __device__ __forceinline__ Reader(const void* tensor, long long stride, long long row, int, const At& me)
       : next(static_cast<const uint8_t*>(tensor) + (row * stride + me.first) * (long long)sizeof(T)) {}
-  __device__ __forceinline__ static uint32_t place(uint32_t memory, const Place<V, C>&) { return memory + threadIdx.x * 16; }
-  // to: the turn's shared memory, this thread's place in it.
-  __device__ __forceinline__ void ask(const void* tensor, uint32_t to, const Place<V, C>& me, const uint32_t (&bytes)[C], bool has,
+  __device__ __forceinline__ static uint32_t place(uint32_t memory, const At&) { return memory + threadIdx.x * 16; }
+  // to: the turn's shared memory, this thread's place in it; has: there is such a row; more: and another one after it.
+  __device__ __forceinline__ void ask(const void* tensor, uint32_t to, const At& me, const uint32_t (&bytes)[C], bool has, bool more,
                                       long long step) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const uint32_t n = has ? bytes[c] : 0u;
-      copy_async(to + c * kWarps * 32 * 16, n != 0 ? next + c * me.apart * (int)sizeof(T) : static_cast<const uint8_t*>(tensor), n);
+      const uint32_t n = has ? bytes[c] : 0u;  // (0: the address is not read)
+      copy_async(to + c * kWarps * 32 * 16, next + (c > 0 && bytes[c] == 0 ? 0 : c * me.apart() * (int)sizeof(T)), n);
     }
-    next += step;
+    if (more) next += step;
   }
-  __device__ __forceinline__ void load(uint32_t from, const Place<V, C>&, int c, long long, typename P::L (&f)[P::N]) const {
+  __device__ __forceinline__ void load(uint32_t from, const At&, int c, typename P::L (&f)[P::N]) const {
     P::load(from + c * kWarps * 32 * 16, f);
   }
+  __device__ __forceinline__ void advance(long long) {}
 };
 
 // Words: the lanes of a row copy the granules of their C row_lanes columns or pairs of columns (and one more: they may begin in
 // the middle of a granule); a lane reads other lanes' copies, so a warp meets (__syncwarp) between copies and reads.
-template <typename T, int V, int C, int kDepth, int kWarps>
-struct Reader<T, V, C, kDepth, kWarps, false> {
+template <typename T, int V, int C, int kWarps, bool kWide>
+struct Reader<T, V, C, kWarps, kWide, false> {
   using P = Piece<T, V>;
+  using At = Place<V, C, kWide>;
   static constexpr int kWarp = (8 * C + 8) * 16;  // a warp's: C / 4 granules a lane, and one more for each of up to 8 rows
   static constexpr int kTurn = kWarps * kWarp;
   const uint8_t* next;  // the warp's first column in the row to be asked for next
-  int left;             // bytes of the row from there on
+  uint32_t src;         // the same of the row to be loaded next, mod 2^32
+  int left;             // bytes of a row from there on
 
-  __device__ __forceinline__ Reader(const void* tensor, long long stride, long long row, int width, const Place<V, C>& me) {
+  __device__ __forceinline__ Reader(const void* tensor, long long stride, long long row, int width, const At& me) {
     const int first = me.row_warp * C * 32 * V;
     next = static_cast<const uint8_t*>(tensor) + (row * stride + first) * (long long)sizeof(T);
+    src = (uint32_t)reinterpret_cast<uintptr_t>(next);
     left = max(width - first, 0) * (int)sizeof(T);
   }
-  __device__ __forceinline__ static uint32_t place(uint32_t memory, const Place<V, C>& me) {
-    return memory + (threadIdx.x >> 5) * kWarp + me.sub * (me.row_lanes * (C / 4) + 1) * 16;
+  __device__ __forceinline__ static uint32_t place(uint32_t memory, const At& me) {
+    return memory + (threadIdx.x >> 5) * kWarp + me.sub * (me.row_lanes() * (C / 4) + 1) * 16;
   }
-  __device__ __forceinline__ void granule(const void* tensor, uint32_t to, const uint8_t* start, int lead, int g, int n) const {
-    const int size = min(max(n + lead - 16 * g, 0), 16);
-    const uint8_t* src = start + 16 * g;
-    if (size > 0 && src < tensor) {  // (the tensor's first row: a granule that begins in front of it)
-#pragma unroll 1
-      for (int i = 0; i < 16; i += (int)sizeof(T)) {
-        const bool in = src + i >= tensor && i < size;
-        if constexpr (sizeof(T) == 4) {
-          const uint32_t v = in ? *reinterpret_cast<const uint32_t*>(src + i) : 0u;
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 16 * g + i), "r"(v) : "memory");
-        } else {
-          const uint16_t v = in ? *reinterpret_cast<const uint16_t*>(src + i) : (uint16_t)0;
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 16 * g + i), "h"(v) : "memory");
-        }
+  __device__ __forceinline__ void ask(const void* tensor, uint32_t to, const At& me, const uint32_t (&)[C], bool has, bool more,
+                                      long long step) {
+    const int lead = (int)(reinterpret_cast<uintptr_t>(next) & 15u), n = has ? left + lead : 0;
+    const uint8_t* start = next - lead;
+    const bool front = has && start < tensor;  // the tensor's first row begins in the middle of a granule
+#pragma unroll
+    for (int k = 0; k <= C / 4; ++k) {
+      const int g = k < C / 4 ? k * me.row_lanes() + me.lane : C / 4 * me.row_lanes();
+      const int size = min(max(n - 16 * g, 0), 16);
+      if ((k < C / 4 || me.lane == 0) && !(front && g == 0)) copy_async(to + 16 * g, start + (size > 0 ? 16 * g : 0), (uint32_t)size);
+    }
+    if (front && me.lane == 0) first_granule(tensor, to, start, n);
+    if (more) next += step;
+  }
+  // Its elements of the row one by one, and zeros.
+  __device__ __noinline__ static void first_granule(const void* tensor, uint32_t to, const uint8_t* start, int n) {
+    for (int i = 0; i < 16; i += (int)sizeof(T)) {
+      const bool in = start + i >= tensor && i < n;
+      if constexpr (sizeof(T) == 4) {
+        const uint32_t v = in ? *reinterpret_cast<const uint32_t*>(start + i) : 0u;
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + i), "r"(v) : "memory");
+      } else {
+        const uint16_t v = in ? *reinterpret_cast<const uint16_t*>(start + i) : (uint16_t)0;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + i), "h"(v) : "memory");
       }
-    } else {
-      copy_async(to + 16 * g, size > 0 ? src : start, (uint32_t)size);
     }
   }
-  __device__ __forceinline__ void ask(const void* tensor, uint32_t to, const Place<V, C>& me, const uint32_t (&)[C], bool has,
-                                      long long step) {
-    const int lead = (int)(reinterpret_cast<uintptr_t>(next) & 15u), n = has ? left : -16;
-    const uint8_t* start = next - lead;
-#pragma unroll
-    for (int k = 0; k < C / 4; ++k) granule(tensor, to, start, lead, k * me.row_lanes + me.lane, n);
-    if (me.lane == 0) granule(tensor, to, start, lead, C / 4 * me.row_lanes, n);
-    next += step;
+  __device__ __forceinline__ void load(uint32_t from, const At& me, int c, typename P::L (&f)[P::N]) const {
+    P::load(from + (src & 12u) + (c * me.row_lanes() + me.lane) * 4, src, f);
   }
-  __device__ __forceinline__ void load(uint32_t from, const Place<V, C>& me, int c, long long step, typename P::L (&f)[P::N]) const {
-    const uint32_t src = (uint32_t)reinterpret_cast<uintptr_t>(next) - kDepth * (uint32_t)step;  // (where the row came from)
-    P::load(from + (src & 12u) + (c * me.row_lanes + me.lane) * 4, src, f);
-  }
+  __device__ __forceinline__ void advance(long long step) { src += (uint32_t)step; }
 };
 
 __device__ __forceinline__ void group_sync(int group, int warps) {
@@ -350,8 +365,8 @@ inline bool on16(const void* p, long long stride_bytes) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)stride_bytes) & 15u) == 0;
 }
 
-// A row of `width` over lanes of E columns in vectors of V.
-inline Plan make_plan(int width, int v, int e, int warps) {
+// A row of `width` over lanes of e columns.
+inline Plan make_plan(int width, int e, int warps) {
   Plan p = {};
   const int threads = (width + e - 1) / e;  // of a row
   p.row_warps = (threads + 31) / 32;
