@@ -227,32 +227,49 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = me.column(c);
+      if constexpr (V >= 4) {  // whole vectors, at multiples of 16 bytes
+        if (bytes[c] == 0) continue;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        if constexpr (V == 1) {
-          if (col < a.width) {
-            to[col] = aw[c][e];
-            to[a.width + col] = ab[c][e];
-          }
-        } else {
-          const int at = col + 2 * e;
-          float lo, hi;
-          f2_unpack(aw[c][e], lo, hi);
-          if (at < a.width) to[at] = lo;
-          if (at + 1 < a.width) to[at + 1] = hi;
-          f2_unpack(ab[c][e], lo, hi);
-          if (at < a.width) to[a.width + at] = lo;
-          if (at + 1 < a.width) to[a.width + at + 1] = hi;
+        for (int e = 0; e < N; e += 2) {
+          float4 v;
+          f2_unpack(aw[c][e], v.x, v.y);
+          f2_unpack(aw[c][e + 1], v.z, v.w);
+          *reinterpret_cast<float4*>(to + col + 2 * e) = v;
+          f2_unpack(ab[c][e], v.x, v.y);
+          f2_unpack(ab[c][e + 1], v.z, v.w);
+          *reinterpret_cast<float4*>(to + a.width + col + 2 * e) = v;
         }
+      } else if constexpr (V == 2) {
+        float lo, hi;
+        f2_unpack(aw[c][0], lo, hi);
+        if (col < a.width) to[col] = lo;
+        if (col + 1 < a.width) to[col + 1] = hi;
+        f2_unpack(ab[c][0], lo, hi);
+        if (col < a.width) to[a.width + col] = lo;
+        if (col + 1 < a.width) to[a.width + col + 1] = hi;
+      } else if (col < a.width) {
+        to[col] = aw[c][0];
+        to[a.width + col] = ab[c][0];
       }
     }
   }
   __syncthreads();
   float* to = p.cluster > 0 ? sums : a.partial + (long long)blockIdx.x * 2 * a.width;  // (in a cluster: the first group's place)
-  for (int c = threadIdx.x; c < 2 * a.width; c += kThreads) {
-    float t = 0.0f;
-    for (int g = 0; g < p.groups; ++g) t += sums[(size_t)g * 2 * a.width + c];
-    to[c] = t;
+  if constexpr (V >= 4) {
+    for (int c = threadIdx.x * 4; c < 2 * a.width; c += kThreads * 4) {
+      float4 t = *reinterpret_cast<const float4*>(sums + c);
+      for (int g = 1; g < p.groups; ++g) {
+        const float4 v = *reinterpret_cast<const float4*>(sums + (size_t)g * 2 * a.width + c);
+        t = make_float4(t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w);
+      }
+      *reinterpret_cast<float4*>(to + c) = t;
+    }
+  } else {
+    for (int c = threadIdx.x; c < 2 * a.width; c += kThreads) {
+      float t = sums[c];
+      for (int g = 1; g < p.groups; ++g) t += sums[(size_t)g * 2 * a.width + c];
+      to[c] = t;
+    }
   }
   if (p.cluster == 0) return;
   // The cluster is all CTAs of the set: each adds up its share of the columns.
@@ -279,30 +296,38 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
   cluster_sync();  // nobody leaves while its sums are being read
 }
 
-// dweight and dbias: the sums of the CTAs' parts [set][part][2][width].  A CTA takes 32 of the 2 width columns, its 8 warps
-// every 8th part each, and adds the warps up in order.  both: the two go to one row, added.
-__global__ void __launch_bounds__(256) norm_sum_kernel(const float* __restrict__ partial, int parts, int width, float* dweight,
-                                                       float* dbias, long long sum_gstride, int blocks) {
-  __shared__ float sums[8][33];
-  grid_dep_wait();
-  grid_dep_launch();
+// dweight and dbias: the sums of the CTAs' parts [set][part][2][width].  A CTA takes 32 of the 2 width columns, its 16 warps
+// every 16th part each (with up to 160 parts all loads at once: the kernel is one trip to the L2 cache), and adds the warps up
+// in order.  both: the two go to one row, added.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const float* __restrict__ partial, int parts, int width,
+                                                                  float* dweight, float* dbias, long long sum_gstride, int blocks) {
+  __shared__ float sums[kSumWarps][33];
   const int set = blockIdx.x / blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = (blockIdx.x - set * blocks) * 32 + lane;
   const bool both = dweight == dbias;
+  const float* p = partial + ((long long)set * parts + warp) * 2 * width + c;
   float t = 0.0f;
+  grid_dep_wait();
+  grid_dep_launch();
   if (c < (both ? width : 2 * width)) {
-    const float* p = partial + (long long)set * parts * 2 * width + c;
-#pragma unroll 4
-    for (int i = warp; i < parts; i += 8) {
-      t += p[(long long)i * 2 * width];
-      if (both) t += p[(long long)i * 2 * width + width];
+    for (int i = warp; i < parts; i += 10 * kSumWarps, p += 10LL * kSumWarps * 2 * width) {
+      float v[10], u[10];
+#pragma unroll
+      for (int k = 0; k < 10; ++k) {
+        const bool in = i + k * kSumWarps < parts;
+        v[k] = in ? __ldg(p + (long long)k * kSumWarps * 2 * width) : 0.0f;
+        u[k] = in && both ? __ldg(p + (long long)k * kSumWarps * 2 * width + width) : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 10; ++k) t += v[k] + u[k];
     }
   }
   sums[warp][lane] = t;
   __syncthreads();
   if (warp != 0) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) t += sums[i][lane];
+  for (int i = 1; i < kSumWarps; ++i) t += sums[i][lane];
   const long long at = set * sum_gstride;
   if (c < width) {
     if (dweight != nullptr) dweight[at + c] = t;
@@ -359,7 +384,7 @@ cudaError_t norm_bwd_run(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
   }
   if (!second) return cudaSuccess;
   const int blocks = ((a.dweight == a.dbias ? 1 : 2) * a.width + 31) / 32;
-  return launch_kernel(norm_sum_kernel, dim3(blocks * a.groups), dim3(256), 0, s, true, (const float*)a.partial, parts, a.width,
+  return launch_kernel(norm_sum_kernel, dim3(blocks * a.groups), dim3(kSumWarps * 32), 0, s, true, (const float*)a.partial, parts, a.width,
                        a.dweight, a.dbias, a.sum_gstride, blocks);
 }
 
