@@ -195,20 +195,24 @@ def _on_current(t: torch.Tensor, name: str) -> int:
     return device
 
 
+def _row_stride(t: torch.Tensor, width: int, name: str) -> int:
+    """Elements between the rows of a tensor that is contiguous, or two-dimensional with rows some way apart."""
+    if t.is_contiguous():
+        return width
+    if t.dim() != 2 or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    return t.stride(0)
+
+
 def _rows(t: torch.Tensor, dtype, rows: int, width: int, name: str, device: int):
-    """Address and row stride (elements) of a tensor of `rows` rows of `width`: contiguous, or two-dimensional with
-    rows some way apart."""
+    """Address and row stride of a tensor of `rows` rows of `width`."""
     if t.shape[-1] != width or t.numel() != rows * width:
         raise ValueError(f"{name} {tuple(t.shape)}: expected {rows} rows of {width}")
     if t.get_device() != device:
         raise ValueError(f"{name} must live on the GPU of the other tensors, cuda:{device}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.is_contiguous():
-        return t.data_ptr(), width
-    if t.dim() != 2 or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), _row_stride(t, width, name)
 
 
 _BF = torch.bfloat16
@@ -505,30 +509,29 @@ def qk_norm_rope_backward(qkv, q_norm_w, k_norm_w, rope_cos, rope_sin, dqp, dkp,
         _sized(ws, torch.uint8, ws.numel(), "ws", d), ws.numel(), _stream(stream, d)))
 
 
-def _norm_types(x, params, name: str) -> int:
-    """mi_dtype of x; params: the first of weight and bias that is given, or None.  Returns both types' codes."""
-    if x.dtype not in _DTYPES:
-        raise TypeError(f"{name}: {x.dtype} is not one of bfloat16, float16, float32")
-    if params is None or params.dtype == x.dtype:
-        return _DTYPES[x.dtype], _DTYPES[x.dtype]
+def _norm_types(dtype, params, name: str):
+    """mi_dtype of a tensor and of its parameters (of the first of weight and bias that is given, or None)."""
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name}: {dtype} is not one of bfloat16, float16, float32")
+    if params is None or params.dtype == dtype:
+        return code, code
     if params.dtype != torch.float32:
-        raise TypeError(f"weight and bias: expected {x.dtype} or torch.float32, got {params.dtype}")
-    return _DTYPES[x.dtype], 2
+        raise TypeError(f"weight and bias: expected {dtype} or torch.float32, got {params.dtype}")
+    return code, 2
 
 
 def layer_norm(x, weight, bias, out, mean=None, rstd=None, eps=1e-6, stream=None):
     """out = (x - m) rstd weight + bias over the last axis of x; mean, rstd (fp32, one a row) for layer_norm_backward.
     x and out: bf16, fp16 or fp32, contiguous or two-dimensional with rows some way apart; weight, bias: x's type or
     fp32, or None."""
-    d, width = _on_current(x, "x"), x.shape[-1]
+    d, width, dtype, f32 = _on_current(x, "x"), x.shape[-1], x.dtype, torch.float32
     rows = x.numel() // width if width else 0
     params = weight if weight is not None else bias
-    dt, pt = _norm_types(x, params, "x")
-    xp, xs = _rows(x, x.dtype, rows, width, "x", d)
-    op, os_ = _rows(out, x.dtype, rows, width, "out", d)
-    f32 = torch.float32
+    dt, pt = _norm_types(dtype, params, "x")
+    op, os_ = _rows(out, dtype, rows, width, "out", d)
     _check(lib().mi_layer_norm(
-        xp, xs, None if weight is None else _sized(weight, params.dtype, width, "weight", d),
+        x.data_ptr(), _row_stride(x, width, "x"), None if weight is None else _sized(weight, params.dtype, width, "weight", d),
         None if bias is None else _sized(bias, params.dtype, width, "bias", d), op, os_,
         None if mean is None else _sized(mean, f32, rows, "mean", d),
         None if rstd is None else _sized(rstd, f32, rows, "rstd", d), rows, width, eps, dt, pt, _stream(stream, d)))
@@ -543,16 +546,15 @@ def layer_norm_backward_workspace_size(rows, width) -> int:
 def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, residual=None, stream=None):
     """Gradients of layer_norm: dx (with `residual`, the gradient that comes past the norm, added; dx may be that tensor),
     and the fp32 sums dweight and dbias (either may be None).  A row whose dy is zero adds nothing, whatever it holds."""
-    d, width = _on_current(dy, "dy"), x.shape[-1]
-    rows, f32 = x.numel() // width if width else 0, torch.float32
-    dt, pt = _norm_types(x, weight, "x")
-    yp, ys = _rows(dy, x.dtype, rows, width, "dy", d)
-    xp, xs = _rows(x, x.dtype, rows, width, "x", d)
-    rp, rs = (None, 0) if residual is None else _rows(residual, x.dtype, rows, width, "residual", d)
-    gp, gs = _rows(dx, x.dtype, rows, width, "dx", d)
+    d, width, dtype, f32 = _on_current(dy, "dy"), dy.shape[-1], dy.dtype, torch.float32
+    rows = dy.numel() // width if width else 0
+    dt, pt = _norm_types(dtype, weight, "dy")
+    xp, xs = _rows(x, dtype, rows, width, "x", d)
+    rp, rs = (None, 0) if residual is None else _rows(residual, dtype, rows, width, "residual", d)
+    gp, gs = _rows(dx, dtype, rows, width, "dx", d)
     ws_bytes = 0 if ws is None else ws.numel()
     _check(lib().mi_layer_norm_backward(
-        yp, ys, xp, xs, None if weight is None else _sized(weight, weight.dtype, width, "weight", d),
+        dy.data_ptr(), _row_stride(dy, width, "dy"), xp, xs, None if weight is None else _sized(weight, weight.dtype, width, "weight", d),
         _sized(mean, f32, rows, "mean", d), _sized(rstd, f32, rows, "rstd", d), rp, rs, gp, gs,
         None if dweight is None else _sized(dweight, f32, width, "dweight", d),
         None if dbias is None else _sized(dbias, f32, width, "dbias", d), rows, width, dt, pt,

@@ -21,8 +21,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Place<V, C, kWide> me(p);
   grid_dep_wait();
-  const long long row0 = (long long)a.rows * blockIdx.x / gridDim.x;
-  const int rows = (int)((long long)a.rows * (blockIdx.x + 1) / gridDim.x - row0);
+  const Share mine_of(a.rows, blockIdx.x, gridDim.x);
+  const long long row0 = mine_of.first;
+  const int rows = mine_of.count;
   const int apart = p.apart;
   int left = me.group < p.groups ? rows - me.group * p.batch : 0;  // rows from the group's next batch on
   long long row = row0 + me.group * p.batch + me.sub;
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
     left -= apart;
     row += apart;
     out += p.step[3];
+    ahead = stage;
     stage = stage == last ? slot0 : stage + kStage;
-    ahead = ahead == last ? slot0 : ahead + kStage;
   }
   copy_wait<0>();
 }

@@ -8,7 +8,9 @@ namespace {
 
 constexpr float kMax = 3.402823466e38f;
 constexpr int kCluster = 8;       // CTAs that sum their rows up in one launch, where rows are few
-constexpr int kClusterTurns = 2;  // turns of their groups up to which that is done
+// Turns of their groups up to which that is done.  (Width 256, us called in turn / replayed from a graph, against two kernels:
+// 74 rows 9.3 / 5.4 against 11.2 / 6.2; 512, two turns, 9.4 / 6.9 against 11.0 / 6.6; 1024, four, 9.5 / 8.4 against 11.0 / 6.7.)
+constexpr int kClusterTurns = 2;
 
 // With g = dy w, n = (x - mean) rstd (rms: x rstd) and the row's sums of g and g (x - mean) (rms: of x^2 and g x):
 //   dx = residual + rstd (g - mean(g) - n mean(g n))   (rms: without mean(g))
@@ -29,8 +31,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
   const Place<V, C, kWide> me(p);
   grid_dep_wait();
   const int set = blockIdx.x / n_parts, part_of_set = blockIdx.x - set * n_parts;
-  const long long row0 = (long long)set * a.seq + (long long)a.seq * part_of_set / n_parts;
-  const int rows = (int)((long long)set * a.seq + (long long)a.seq * (part_of_set + 1) / n_parts - row0);
+  const Share mine_of(a.seq, part_of_set, n_parts);
+  const long long row0 = (long long)set * a.seq + mine_of.first;
+  const int rows = mine_of.count;
   const int apart = p.apart;
   int left = me.group < p.groups ? rows - me.group * p.batch : 0;  // rows from the group's next batch on
   long long row = row0 + me.group * p.batch + me.sub;
@@ -202,8 +205,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
     left -= apart;
     row += apart;
     out += p.step[3];
+    ahead = stage;
     stage = stage == last ? slot0 : stage + kStage;
-    ahead = ahead == last ? slot0 : ahead + kStage;
   }
   copy_wait<0>();
   if (a.dweight == nullptr && a.dbias == nullptr) return;

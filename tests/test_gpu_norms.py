@@ -87,8 +87,8 @@ class Norm:
         self.dx.clean("dx")
 
 
-WIDTHS = [1, 2, 7, 8, 24, 31, 33, 64, 127, 128, 256, 257, 264, 511, 768, 1000, 1155, 1283, 2047, 2048, 2560, 4096, 4104, 5003,
-          8192, 10007, 12288, 16383, 16384]
+WIDTHS = [1, 2, 7, 8, 24, 31, 33, 64, 127, 128, 256, 257, 264, 511, 512, 520, 768, 1000, 1155, 1283, 1536, 1537, 2047, 2048, 2560, 4096,
+          4097, 4104, 5003, 8191, 8192, 8200, 10007, 12288, 16383, 16384]
 
 
 @pytest.mark.parametrize("width", WIDTHS)
