@@ -9,6 +9,11 @@ namespace {
 // mean m and the squares q around it.  Over the warps of a row, A = sum n (m - m_0) and B = sum (q + n (m - m_0)^2) give the
 // row's mean m_0 + A / width and its squares B - A^2 / width.  (What that difference takes off is at most as many times what is
 // left as there are warps, 16: the row's squares are at least n_0 (m_0 - mean)^2, its first warp's.)
+//
+// kBehind: a row's sums over its warps, and its outputs, are one turn behind the warps' own sums and run beside the next row's,
+// which hides most of the shuffles' and the barrier's time (16418 x 4096 bf16 51.5 -> 45.5 us, 8260 x 2560 20.1 -> 19.0).  It takes the
+// registers of a second row: single words and 32 columns a lane do not have them (9237 x 1155 fp32 21.2 -> 27.4 us), and rows of
+// one warp have nothing to wait for (40000 x 256 10.5 -> 10.9).
 template <typename T, int V, int E, int kDepth, int kWarps, bool kWide>
 __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerNormArgs a, const Plan p) {
   using P = Piece<T, V>;
@@ -16,6 +21,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
   constexpr int C = E / V, N = P::N, kThreads = kWarps * 32;
   using In = Reader<T, V, C, kWarps, kWide>;
   constexpr int kStage = In::kTurn;
+  constexpr bool kBehind = kWide && V >= 4 && E == 16;
   extern __shared__ __align__(128) uint8_t memory[];
   __shared__ float2 parts[2][kWarps + 16];  // a warp's mean and squares (read 16 from a group's first on)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -59,12 +65,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
   uint8_t* out = static_cast<uint8_t*>(a.out) + (row * a.out_stride + me.first) * (long long)sizeof(T);
   const uint32_t last = slot0 + (kDepth - 1) * kStage;
   uint32_t stage = slot0, ahead = last;
-  for (int turn = 0; left > 0; turn ^= 1) {
+  auto fetch = [&](L (&x)[C][N], float& s) {  // the row that has come, and the sum of this lane's columns
     if (V < 4) __syncwarp();  // (the warp has read what now makes room)
     ask(ahead);
     copy_wait<kDepth - 1>();
     if (V < 4) __syncwarp();
-    L x[C][N];
     L t = v_of<L>(0.0f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -72,9 +77,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
 #pragma unroll
       for (int e = 0; e < N; ++e) t = v_add(t, x[c][e]);
     }
-    const float s = kWide ? warp_sum(v_sum(t)) : lanes_sum(v_sum(t), p.row_lanes);
-    const float m = s * inv_cols;
-    t = v_of<L>(0.0f);
+    x_in.advance(p.step[0]);
+    ahead = stage;
+    stage = stage == last ? slot0 : stage + kStage;
+    s = v_sum(t);
+  };
+  auto squares = [&](const L (&x)[C][N], float m) {  // of this lane's columns around m
+    L t = v_of<L>(0.0f);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const L nm = bytes[c] == V * sizeof(T) ? v_of<L>(-m) : V == 2 && bytes[c] == sizeof(T) ? v_of2<L>(-m, 0.0f) : v_of<L>(0.0f);
@@ -84,18 +93,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
         t = v_fma(d, d, t);
       }
     }
-    float mean = m, square = kWide ? warp_sum(v_sum(t)) : lanes_sum(v_sum(t), p.row_lanes);
-    if constexpr (kWide) {
-      if (lane == 0) parts[turn][warp] = make_float2(m, square);
-      group_sync(me.group, p.row_warps);
-      const float first = parts[turn][me.group * p.row_warps].x;
-      const float2 part = parts[turn][me.group * p.row_warps + (lane & 15)];
-      const float d = part.x - first, nd = n_of_lane * d;
-      const float v = lane < 16 ? nd : fmaf(nd, d, part.y);
-      const float2 both = warps_sum2((lane & 15) < p.row_warps ? v : 0.0f);
-      mean = fmaf(both.x, inv, first);
-      square = fmaf(-both.x * inv, both.x, both.y);
-    }
+    return v_sum(t);
+  };
+  // The lane's part of a row's sums over its warps (see above), from the turn's parts.
+  float first = 0.0f;
+  auto joined = [&](int turn) {
+    first = parts[turn][me.group * p.row_warps].x;
+    const float2 part = parts[turn][me.group * p.row_warps + (lane & 15)];
+    const float d = part.x - first, nd = n_of_lane * d;
+    const float v = lane < 16 ? nd : fmaf(nd, d, part.y);
+    return (lane & 15) < p.row_warps ? v : 0.0f;
+  };
+  auto write = [&](const L (&x)[C][N], float mean, float square) {
     const float rstd = rsqrtf(fmaf(square, inv, a.eps));
     const bool mine = me.sub < left;
     const L nm = v_of<L>(-mean), rs = v_of<L>(rstd);
@@ -110,12 +119,61 @@ __global__ void __launch_bounds__(kWarps * 32, 1) layer_norm_kernel(const LayerN
       if (a.mean != nullptr) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
-    x_in.advance(p.step[0]);
     left -= apart;
     row += apart;
     out += p.step[3];
-    ahead = stage;
-    stage = stage == last ? slot0 : stage + kStage;
+  };
+  float m, q;  // a row's, as this warp has it
+  if constexpr (kBehind) {
+    auto share = [&](int turn) {
+      if (lane == 0) parts[turn][warp] = make_float2(m, q);
+      group_sync(me.group, p.row_warps);
+    };
+    auto turn_of = [&](int turn, const L (&x)[C][N], L (&next)[C][N]) {
+      float s;
+      fetch(next, s);
+      float v = joined(turn);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (o < 16) v += __shfl_xor_sync(0xffffffffu, v, o);
+      }
+      const float u = __shfl_xor_sync(0xffffffffu, v, 16);
+      const float sum = lane < 16 ? v : u, more = lane < 16 ? u : v;
+      m = s * inv_cols;
+      q = warp_sum(squares(next, m));
+      write(x, fmaf(sum, inv, first), fmaf(-sum * inv, sum, more));
+      share(turn ^ 1);
+    };
+    L even[C][N], odd[C][N];
+    if (left > 0) {
+      fetch(even, m);
+      m = warp_sum(m) * inv_cols;
+      q = warp_sum(squares(even, m));
+      share(0);
+    }
+    while (left > 0) {
+      turn_of(0, even, odd);
+      if (left <= 0) break;
+      turn_of(1, odd, even);
+    }
+  } else {
+    for (int turn = 0; left > 0; turn ^= 1) {
+      L x[C][N];
+      float s;
+      fetch(x, s);
+      m = (kWide ? warp_sum(s) : lanes_sum(s, p.row_lanes)) * inv_cols;
+      s = squares(x, m);
+      q = kWide ? warp_sum(s) : lanes_sum(s, p.row_lanes);
+      if constexpr (kWide) {
+        if (lane == 0) parts[turn][warp] = make_float2(m, q);
+        group_sync(me.group, p.row_warps);
+        const float2 both = warps_sum2(joined(turn));
+        m = fmaf(both.x, inv, first);
+        q = fmaf(-both.x * inv, both.x, both.y);
+      }
+      write(x, m, q);
+    }
   }
   copy_wait<0>();
 }
