@@ -17,6 +17,11 @@ constexpr int kClusterTurns = 2;
 //   sums over rows: dweight += dy n, dbias += dy.
 // A row whose sums or statistics are not finite is looked at again: if its dy is zero it counts as absent (so what
 // padding holds reaches nothing), which costs rows that are finite nothing.
+//
+// Without the sums over rows the loop runs at 0.98 of the measured copy rate (33040 x 2560 with a residual 104 us, the copies'
+// floor 101); adding them up costs 4 us a call.  A row's sums one turn behind, beside the next row's, as in the forward, gained
+// nothing: the registers of a second row are not there, and reading the row from shared memory again costs as much as it
+// hides (8260 x 2560 35.0 against 33.9 us, 3 x 10571 x 1792 rms 69.3 against 65.0).
 template <typename T, int V, int E, int kDepth, int kWarps, bool kWide, bool kRms, bool kResidual>
 __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdArgs a, const Plan p, int n_parts) {
   using P = Piece<T, V>;
