@@ -199,7 +199,8 @@ cudaError_t layer_norm_run(const LayerNormArgs& a, int num_sms, cudaStream_t s) 
   return layer_norm_start<T, V, E, kWarps, true>(a, p, grid, s);
 }
 
-// Columns of a lane: 16 (40 M bf16 elements: 31 us at width 256, 35 at 2560, 34 at 4096; with 8 and 24 warps 34, 43, 47), but 8
+// Columns of a lane (figures of one build, with more rows on the way than now): 16 (40 M bf16 elements: 31 us at width 256, 35 at
+// 2560, 34 at 4096; with 8 and 24 warps 34, 43, 47), but 8
 // in odd rows while a CTA of 24 warps holds two of them (20 M: 49 against 50 us at width 1023, 51 against 49 at 2047), and 32
 // where 16 warps of 16 columns a lane do not hold a row.
 template <typename T, int V>

@@ -397,7 +397,7 @@ cudaError_t norm_bwd_run(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
 }
 
 // Columns of a lane: the fewer registers a row takes, the more warps there can be.  rms: 8 with 24 warps (40 M elements with a
-// residual: 59 us at width 3072, 60 at 2560; with 16 and 16 warps 67, 66).  Layer norm: 16 (61 us at 2560, 62 at 4096; with 8
+// residual: 61 us at width 1536, 60 at 2560; with 16 and 16 warps 65, 66).  Layer norm: 16 (61 us at 2560, 62 at 4096; with 8
 // 65, 71), in odd rows 8 (20 M, no residual: 70 us at width 1023; with 16 82).  32 where these do not hold a row.
 template <typename T, int V, bool kRms>
 cudaError_t norm_bwd_any(const NormBwdArgs& a, int num_sms, cudaStream_t s) {

@@ -16,7 +16,8 @@
 // Measured on the way (GB300, bf16; 8260 x 2560 backward with a residual / 16418 x 4096 forward, us): one row a CTA at a
 // time from L1 368 / 141; rows by bulk copies of one thread a group into a ring with barriers 51 / 64 (the one thread's copies,
 // and every branch, are on the row's chain of about 1400 cycles); sums and outputs as two phases over tiles of rows, each
-// with its own mapping of threads, 56 / 67 (twice the instructions); a lane's own copies 39 / 51.
+// with its own mapping of threads, 56 / 67 (twice the instructions); a lane's own copies 39 / 51; fewer rows on the way and
+// cheaper ends 34 / 46.
 #pragma once
 
 #include <cuda_fp16.h>
