@@ -1148,7 +1148,6 @@ mi_status mi_layer_norm(const void* x, int64_t x_stride, const void* weight, con
   a.eps = eps;
   a.dtype = dtype;
   a.param_dtype = param_dtype;
-  a.err = dev->err;
   cudaError_t e = mi::layer_norm_launch(a, dev->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MI_OK : cuda_fail(e, "layer norm");
 }
@@ -1222,7 +1221,6 @@ mi_status mi_layer_norm_backward(const void* dy, int64_t dy_stride, const void* 
   a.dtype = dtype;
   a.param_dtype = param_dtype;
   a.partial = static_cast<float*>(ws);
-  a.err = dev->err;
   cudaError_t e = mi::norm_bwd_launch(a, dev->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MI_OK : cuda_fail(e, "layer norm backward");
 }
@@ -1285,7 +1283,6 @@ mi_status mi_mod_rmsnorm_backward(const void* dy, const void* x, const void* mod
   a.rms = true;
   a.dtype = a.param_dtype = MI_BF16;
   a.partial = static_cast<float*>(ws);
-  a.err = dev->err;
   cudaError_t e = mi::norm_bwd_launch(a, dev->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MI_OK : cuda_fail(e, "mod_rmsnorm backward");
 }

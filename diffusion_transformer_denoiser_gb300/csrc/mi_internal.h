@@ -144,7 +144,6 @@ struct LayerNormArgs {
   float eps;
   int dtype, param_dtype;
   bool param_vec;              // (set by the launch) the parameters are on 16-byte boundaries
-  int* err;
 };
 cudaError_t layer_norm_launch(const LayerNormArgs& a, int num_sms, cudaStream_t s);
 
@@ -171,7 +170,6 @@ struct NormBwdArgs {
   int dtype, param_dtype;
   bool param_vec;              // (set by the launch) every group's weight is on a 16-byte boundary
   float* partial;              // norm_bwd_workspace() bytes
-  int* err;
 };
 size_t norm_bwd_workspace(int groups, int seq, int width, int num_sms);
 cudaError_t norm_bwd_launch(const NormBwdArgs& a, int num_sms, cudaStream_t s);
