@@ -196,18 +196,19 @@ cudaError_t layer_norm_run(const LayerNormArgs& a, int num_sms, cudaStream_t s) 
   const int grid = need < num_sms ? (int)need : num_sms;
   if constexpr (E == 8 || (E == 16 && V >= 4))  // (wider pieces come with wide rows only)
     if (p.row_warps == 1) return layer_norm_start<T, V, E, kWarps, false>(a, p, grid, s);
+  if (!wide_plan(p)) return cudaErrorInvalidConfiguration;
   return layer_norm_start<T, V, E, kWarps, true>(a, p, grid, s);
 }
 
-// Columns of a lane (figures of one build, with more rows on the way than now): 16 (40 M bf16 elements: 31 us at width 256, 35 at
-// 2560, 34 at 4096; with 8 and 24 warps 34, 43, 47), but 8
-// in odd rows while a CTA of 24 warps holds two of them (20 M: 49 against 50 us at width 1023, 51 against 49 at 2047), and 32
-// where 16 warps of 16 columns a lane do not hold a row.
+// Columns of a lane and warps of a CTA: 16 with 16 (40 M bf16 elements: 30 us at widths 256, 2560 and 4096; 8 with 24 warps, without the
+// turn behind, 30, 39, 43).  Odd rows of 16 bits: 8 with 24 up to six warps of them (16 M: width 515 35 / 40 us, 1155 30 / 32,
+// 1535 27 / 27); of fp32: up to three (515 33 / 36; 771 27 with 16 columns, 30 with 8; 1283 26 / 28).  32 where 16 warps of 16
+// columns a lane do not hold a row.
 template <typename T, int V>
 cudaError_t layer_norm_any(const LayerNormArgs& a, int num_sms, cudaStream_t s) {
   if (a.width > 16 * 32 * 16) return layer_norm_run<T, V, 32, 16>(a, num_sms, s);
   if constexpr (V < 4)
-    if (a.width <= 12 * 32 * 8 / 2) return layer_norm_run<T, V, 8, 24>(a, num_sms, s);
+    if (a.width <= (V == 1 ? 3 : 6) * 32 * 8) return layer_norm_run<T, V, 8, 24>(a, num_sms, s);
   return layer_norm_run<T, V, 16, 16>(a, num_sms, s);
 }
 

@@ -18,10 +18,10 @@ constexpr int kClusterTurns = 2;
 // A row whose sums or statistics are not finite is looked at again: if its dy is zero it counts as absent (so what
 // padding holds reaches nothing), which costs rows that are finite nothing.
 //
-// Without the sums over rows the loop runs at 0.98 of the measured copy rate (33040 x 2560 with a residual 104 us, the copies'
-// floor 101); adding them up costs 4 us a call.  A row's sums one turn behind, beside the next row's, as in the forward, gained
+// Without the sums over rows the loop runs at 0.98 of the measured copy rate (33040 x 2560 with a residual 103 us, the copies'
+// floor 101); adding them up costs 4 to 5 us a call.  A row's sums one turn behind, beside the next row's, as in the forward, gained
 // nothing: the registers of a second row are not there, and reading the row from shared memory again costs as much as it
-// hides (8260 x 2560 35.0 against 33.9 us, 3 x 10571 x 1792 rms 69.3 against 65.0).
+// hides (8260 x 2560 35.0 against 33.9 us; with 8 columns a lane 3 x 10571 x 1792 rms 69.3 against 65.0).
 template <typename T, int V, int E, int kDepth, int kWarps, bool kWide, bool kRms, bool kResidual>
 __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdArgs a, const Plan p, int n_parts) {
   using P = Piece<T, V>;
@@ -366,6 +366,7 @@ template <typename T, int V, int E, int kWarps, bool kRms, bool kResidual>
 cudaError_t norm_bwd_width(const NormBwdArgs& a, const Plan& p, int parts, bool sums, cudaStream_t s) {
   if constexpr (E == 8 || (E == 16 && V >= 4))  // (wider pieces come with wide rows only)
     if (p.row_warps == 1) return norm_bwd_start<T, V, E, kWarps, false, kRms, kResidual>(a, p, parts, sums, s);
+  if (!wide_plan(p)) return cudaErrorInvalidConfiguration;
   return norm_bwd_start<T, V, E, kWarps, true, kRms, kResidual>(a, p, parts, sums, s);
 }
 
@@ -396,17 +397,22 @@ cudaError_t norm_bwd_run(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
                        a.dweight, a.dbias, a.sum_gstride, blocks);
 }
 
-// Columns of a lane: the fewer registers a row takes, the more warps there can be.  rms: 8 with 24 warps (40 M elements with a
-// residual: 61 us at width 1536, 60 at 2560; with 16 and 16 warps 65, 66).  Layer norm: 16 (61 us at 2560, 62 at 4096; with 8
-// 65, 71), in odd rows 8 (20 M, no residual: 70 us at width 1023; with 16 82).  32 where these do not hold a row.
+// Columns of a lane and warps of a CTA: 16 with 16, so that few warps meet for a row (40 M elements, us; layer norm with a
+// residual: width 2560 55 against 72 for 8 with 16, 4096 56 / 62; rms without: 2560 43 against 49 for 8 with 24, 4096 44 / 55).
+// rms: 8 with 24 where 16 would leave a quarter of the warps without a row and there is a residual's memory traffic to hide it
+// (width 2816 60 / 64, 3072 55 / 57; without a residual 53 / 51, 47 / 45).  Odd rows of 16 bits: 8 up to three warps of them (16 M: width 515
+// 47 / 49, with a residual 56 / 65), then 16 (769 37 / 44, 1283 36 / 45, with one 43 / 53); of fp32: 8, whose copies leave room
+// for more rows on the way.  32 where these do not hold a row.
 template <typename T, int V, bool kRms>
 cudaError_t norm_bwd_any(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
   if constexpr (kRms) {
-    return norm_bwd_run<T, V, 8, 24, true>(a, num_sms, s);  // (at most 4096 columns: 16 warps)
+    if (a.residual != nullptr && a.width > 5 * 32 * 16 && a.width <= 6 * 32 * 16)
+      return norm_bwd_run<T, V, 8, 24, true>(a, num_sms, s);
+    return norm_bwd_run<T, V, 16, 16, true>(a, num_sms, s);
   } else {
     if (a.width > 16 * 32 * 16) return norm_bwd_run<T, V, 32, 16, false>(a, num_sms, s);
     if constexpr (V < 4)
-      if (a.width <= 16 * 32 * 8) return norm_bwd_run<T, V, 8, 16, false>(a, num_sms, s);
+      if (a.width <= (V == 2 ? 3 : 16) * 32 * 8) return norm_bwd_run<T, V, 8, 16, false>(a, num_sms, s);
     return norm_bwd_run<T, V, 16, 16, false>(a, num_sms, s);
   }
 }

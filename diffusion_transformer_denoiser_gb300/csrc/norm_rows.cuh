@@ -334,6 +334,10 @@ struct Reader<T, V, C, kWarps, kWide, false> {
   __device__ __forceinline__ void advance(long long step) { src += (uint32_t)step; }
 };
 
+// The groups of a kernel with kWide meet at barriers 1 to groups, of 16 that there are: rows of one warp, which need none, have
+// kernels without it.
+constexpr int kBarriers = 16;
+
 __device__ __forceinline__ void group_sync(int group, int warps) {
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
 }
@@ -388,6 +392,9 @@ inline Plan make_plan(int width, int e, int warps) {
   p.apart = p.groups * p.batch;
   return p;
 }
+
+// Whether a kernel with kWide can run the plan.
+inline bool wide_plan(const Plan& p) { return p.row_warps > 1 && p.row_warps <= 16 && p.groups > 0 && p.groups < kBarriers; }
 
 // Turns in shared memory: as many as keep 48 KB on the way per SM.  What all SMs ask for at the start comes in any order, so
 // more makes the first rows late and gains nothing later (us with 32, 48, 64, 96, 128 KB: 4130 x 2560 forward 12.1, 12.4, 12.6, 13.5,
