@@ -398,7 +398,8 @@ inline bool wide_plan(const Plan& p) { return p.row_warps > 1 && p.row_warps <= 
 
 // Turns in shared memory: as many as keep 48 KB on the way per SM.  What all SMs ask for at the start comes in any order, so
 // more makes the first rows late and gains nothing later (us with 32, 48, 64, 96, 128 KB: 4130 x 2560 forward 12.1, 12.4, 12.6, 13.5,
-// 14.0; 16418 x 4096 50.9, 51.5, 51.6, 52.8, 53.0; 3 x 10571 x 1792 rms backward 65.3, 65.2, 63.9, 64.7, 66.5).
+// 14.0; 16418 x 4096 50.9, 51.5, 51.6, 52.8, 53.0; 3 x 10571 x 1792 rms backward, then with 8 columns a lane,
+// 65.3, 65.2, 63.9, 64.7, 66.5).
 constexpr int kFlight = 48 * 1024;
 constexpr int depth_of(int inputs, int turn, int held = 0) {  // held: rows that are kept beside the one that has come
   const int want = 1 + held + (kFlight + inputs * turn - 1) / (inputs * turn), fit = kRingBytes / (inputs * turn);

@@ -110,6 +110,18 @@ def test_layer_norm_backward(width, kind, weights):
         n.check_backward()
 
 
+@pytest.mark.parametrize("width", [255, 513, 767, 769, 1023, 1025, 1535, 1791, 4095])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+def test_odd_rows_where_the_layout_changes(width, kind):
+    mi = require_gpu()
+    for residual in (False, True):
+        n = Norm(629, width, kind, residual=residual)
+        n.check_forward(mi)
+        n.statistics()
+        n.backward(mi)
+        n.check_backward()
+
+
 @pytest.mark.parametrize("rows,width,kind", [(4130, 2560, "bf16"), (16418, 256, "bf16"), (100003, 40, "f16"), (9237, 1155, "f32"),
                                              (4503, 1283, "f16"), (20011, 33, "bf16"), (3001, 4096, "f32")])
 def test_many_rows(rows, width, kind):
@@ -334,6 +346,15 @@ def test_mod_backward(batch, seq, hidden):
     mi = require_gpu()
     for residual in (True, False):
         m = Mod(batch, seq, hidden, residual)
+        m.backward(mi)
+        m.check()
+
+
+@pytest.mark.parametrize("hidden", [768, 1024, 2304, 2816, 3328, 3840])
+def test_mod_backward_where_the_layout_changes(hidden):
+    mi = require_gpu()
+    for residual in (True, False):
+        m = Mod(2, 701, hidden, residual)
         m.backward(mi)
         m.check()
 
