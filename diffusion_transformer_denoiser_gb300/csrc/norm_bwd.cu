@@ -15,8 +15,11 @@ constexpr int kClusterTurns = 2;
 // With g = dy w, n = (x - mean) rstd (rms: x rstd) and the row's sums of g and g (x - mean) (rms: of x^2 and g x):
 //   dx = residual + rstd (g - mean(g) - n mean(g n))   (rms: without mean(g))
 //   sums over rows: dweight += dy n, dbias += dy.
-// A row whose sums or statistics are not finite is looked at again: if its dy is zero it counts as absent (so what
-// padding holds reaches nothing), which costs rows that are finite nothing.
+// A row whose sums or statistics are not finite, and with given statistics one whose two sums are both zero, is looked at
+// again: if its dy is zero it counts as absent, so what padding holds reaches nothing.  (A dy of zeros gives sums of 0 or NaN.
+// With finite x and statistics n may still overflow and dy n be NaN; an rms norm makes its own r, and x r stays finite.)
+// Rows with a gradient pay two comparisons (8260 x 2560 bf16 with a residual 32.4 us on the device with and without them); a batch that
+// is all padding 33.2 instead of 32.6, 4503 x 1283 fp16 18.9 instead of 17.7.
 //
 // Without the sums over rows the loop runs at 0.98 of the measured copy rate (33040 x 2560 with a residual 103 us, the copies'
 // floor 101); adding them up costs 4 to 5 us a call.  A row's sums one turn behind, beside the next row's, as in the forward, gained
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
     }
     if (kRms) rstd = rsqrtf(fmaf(s1, inv, a.eps));
     float c1 = kRms ? 0.0f : s1 * inv, c2 = s2 * rstd * inv;
-    bool gone = !(fabsf((c1 + c2) + (rstd + mean)) <= kMax);
+    bool gone = !(fabsf((c1 + c2) + (rstd + mean)) <= kMax) || (!kRms && s1 == 0.0f && s2 == 0.0f);
     if (kWide ? gone : (bool)__any_sync(0xffffffffu, gone)) {  // does the row have a gradient at all?
       bool any = false;
 #pragma unroll
