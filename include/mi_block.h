@@ -420,8 +420,10 @@ typedef enum mi_dtype {
  *   weight, bias  [width] of type `dtype` or MI_F32 (param_dtype), or NULL: 1 and 0
  *   mean, rstd  fp32 [rows], for mi_layer_norm_backward, or NULL
  * 1 <= width <= MI_NORM_MAX_WIDTH; rows may be 0 (nothing happens).  The row's mean is taken off before it is
- * squared, in fp32, so a row far from zero loses nothing; a row with an infinity or NaN gives NaN.  Outputs that
- * overlap x, the weights or each other are refused (rows that interleave without touching are fine). */
+ * squared, and what its rounding leaves after it, in fp32, so a row far from zero loses nothing in out and rstd: 100000.1
+ * everywhere gives the bias.  mean itself is rounded to fp32.  Sums and squares are fp32: |x - m| from 2^63 on leaves their range.
+ * A row with an infinity or NaN gives NaN.  Outputs that overlap x, the weights or each other are refused (rows that
+ * interleave without touching are fine). */
 #define MI_NORM_MAX_WIDTH 16384
 mi_status mi_layer_norm(const void* x, int64_t x_stride, const void* weight, const void* bias, void* out, int64_t out_stride,
                         float* mean, float* rstd, int rows, int width, float eps, int dtype, int param_dtype, void* stream);
@@ -430,7 +432,8 @@ mi_status mi_layer_norm(const void* x, int64_t x_stride, const void* weight, con
  *   dx = residual + rstd (g - mean(g) - n mean(g n)),  dweight = sum over rows of dy n,  dbias = sum over rows of dy
  *   residual    [rows, width] of type `dtype` or NULL: the gradient that comes past the norm, added before dx's one
  *               rounding; dx may be the same tensor (same address and stride)
- *   mean, rstd  the forward's
+ *   mean, rstd  the forward's, as given: n is off by what rounding to fp32 has taken from the mean, up to
+ *               2^-24 |mean| rstd
  *   dweight, dbias  fp32 [width] (overwritten, not added to; zeros for no rows), either may be NULL
  * A row whose dy is zero gets dx = residual (or 0) and adds nothing, whatever its x, mean and rstd hold, infinities and
  * NaN included.  Sums over rows have a fixed order.  Other overlaps of an output or the workspace are refused.
