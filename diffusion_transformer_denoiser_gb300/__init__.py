@@ -204,6 +204,13 @@ def _row_stride(t: torch.Tensor, width: int, name: str) -> int:
     return t.stride(0)
 
 
+def _count(n: int, name: str) -> int:
+    """n as the library's int takes it: ctypes would cut the bits above it off."""
+    if not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"{name}={n}: at most {0x7fffffff}")
+    return n
+
+
 def _rows(t: torch.Tensor, dtype, rows: int, width: int, name: str, device: int):
     """Address and row stride of a tensor of `rows` rows of `width`."""
     if t.shape[-1] != width or t.numel() != rows * width:
@@ -527,6 +534,8 @@ def layer_norm(x, weight, bias, out, mean=None, rstd=None, eps=1e-6, stream=None
     fp32, or None."""
     d, width, dtype, f32 = _on_current(x, "x"), x.shape[-1], x.dtype, torch.float32
     rows = x.numel() // width if width else 0
+    if rows > 0x7fffffff:
+        _count(rows, "rows")
     params = weight if weight is not None else bias
     dt, pt = _norm_types(dtype, params, "x")
     op, os_ = _rows(out, dtype, rows, width, "out", d)
@@ -539,7 +548,7 @@ def layer_norm(x, weight, bias, out, mean=None, rstd=None, eps=1e-6, stream=None
 
 def layer_norm_backward_workspace_size(rows, width) -> int:
     n = ctypes.c_size_t()
-    _check(lib().mi_layer_norm_backward_workspace_size(rows, width, ctypes.byref(n)))
+    _check(lib().mi_layer_norm_backward_workspace_size(_count(rows, "rows"), _count(width, "width"), ctypes.byref(n)))
     return n.value
 
 
@@ -548,6 +557,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, resid
     and the fp32 sums dweight and dbias (either may be None).  A row whose dy is zero adds nothing, whatever it holds."""
     d, width, dtype, f32 = _on_current(dy, "dy"), dy.shape[-1], dy.dtype, torch.float32
     rows = dy.numel() // width if width else 0
+    if rows > 0x7fffffff:
+        _count(rows, "rows")
     dt, pt = _norm_types(dtype, weight, "dy")
     xp, xs = _rows(x, dtype, rows, width, "x", d)
     rp, rs = (None, 0) if residual is None else _rows(residual, dtype, rows, width, "residual", d)
@@ -563,7 +574,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws, resid
 
 def mod_rmsnorm_backward_workspace_size(batch, seq, hidden) -> int:
     n = ctypes.c_size_t()
-    _check(lib().mi_mod_rmsnorm_backward_workspace_size(batch, seq, hidden, ctypes.byref(n)))
+    _check(lib().mi_mod_rmsnorm_backward_workspace_size(_count(batch, "batch"), _count(seq, "seq"), _count(hidden, "hidden"),
+                                                        ctypes.byref(n)))
     return n.value
 
 
