@@ -146,7 +146,7 @@ __device__ __forceinline__ double item_squares(const GradEntry& e, uint32_t item
   const uint4* from = reinterpret_cast<const uint4*>(g + t.at) + lane;
   uint4 v[kVectors];
 #pragma unroll
-  for (int k = 0; k < kVectors; ++k) v[k] = k * 32 + lane < t.vectors ? __ldg(from + k * 32) : make_uint4(0, 0, 0, 0);
+  for (int k = 0; k < kVectors; ++k) v[k] = k * 32 + lane < t.vectors ? __ldcg(from + k * 32) : make_uint4(0, 0, 0, 0);
   float edge = 0.0f;  // an element outside of the vectors
   if (lane < t.head) edge = to_f32(g[lane]);
   else if (lane >= 16 && lane - 16 < t.tail) edge = to_f32(g[t.tail_at + lane - 16]);
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) grad_square_kernel(const __gr
 // The norm from n partial sums, the same in every CTA that asks.
 __device__ __forceinline__ float norm_of(const double* partial, int n, double* shared) {
   double t = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) t += __ldg(partial + i);
+  for (int i = threadIdx.x; i < n; i += kThreads) t += __ldcg(partial + i);
   return (float)sqrt(cta_sum(t, shared));
 }
 

@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
   uint8_t* out = static_cast<uint8_t*>(a.dx) + (row * a.dx_stride + me.first) * (long long)sizeof(T);
   float next_mean = 0.0f, next_rstd = 0.0f;
   if (!kRms && me.sub < left) {
-    next_mean = __ldg(a.mean + row);
-    next_rstd = __ldg(a.rstd + row);
+    next_mean = a.mean[row];
+    next_rstd = a.rstd[row];
   }
   const uint32_t last = slot0 + (kDepth - 1) * kStage;
   uint32_t stage = slot0, ahead = last;
@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
     ask(ahead);
     float mean = next_mean, rstd = next_rstd;
     if (!kRms && me.sub < left - apart) {
-      next_mean = __ldg(a.mean + row + apart);
-      next_rstd = __ldg(a.rstd + row + apart);
+      next_mean = a.mean[row + apart];
+      next_rstd = a.rstd[row + apart];
     }
     copy_wait<kDepth - 1>();
     if (V < 4) __syncwarp();
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) norm_bwd_kernel(const NormBwdA
 // every 16th part each (with up to 160 parts all loads at once: the kernel is one trip to the L2 cache), and adds the warps up
 // in order.  both: the two go to one row, added.
 constexpr int kSumWarps = 16;
-__global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const float* __restrict__ partial, int parts, int width,
+__global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const float* partial, int parts, int width,
                                                                   float* dweight, float* dbias, long long sum_gstride, int blocks) {
   __shared__ float sums[kSumWarps][33];
   const int set = blockIdx.x / blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const float* _
 #pragma unroll
       for (int k = 0; k < 10; ++k) {
         const bool in = i + k * kSumWarps < parts;
-        v[k] = in ? __ldg(p + (long long)k * kSumWarps * 2 * width) : 0.0f;
-        u[k] = in && both ? __ldg(p + (long long)k * kSumWarps * 2 * width + width) : 0.0f;
+        v[k] = in ? __ldcg(p + (long long)k * kSumWarps * 2 * width) : 0.0f;
+        u[k] = in && both ? __ldcg(p + (long long)k * kSumWarps * 2 * width + width) : 0.0f;
       }
 #pragma unroll
       for (int k = 0; k < 10; ++k) t += v[k] + u[k];
