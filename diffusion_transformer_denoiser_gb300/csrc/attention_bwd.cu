@@ -152,9 +152,9 @@ __global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const AttnBwdArgs p,
 #pragma unroll
   for (int i = 0; i < kRowHeads; ++i) {
     const bool on = in && h0 + i < p.n_heads;
-    x[i] = on ? __ldg(reinterpret_cast<const uint4*>(p.o + off + i * kHeadDim)) : make_uint4(0, 0, 0, 0);
-    g[i] = on ? __ldg(reinterpret_cast<const uint4*>(p.d_o + off + i * kHeadDim)) : make_uint4(0, 0, 0, 0);
-    l[i] = on ? __ldg(p.lse + ((size_t)b * p.n_heads + h0 + i) * p.seq + s) : -inf();
+    x[i] = on ? *reinterpret_cast<const uint4*>(p.o + off + i * kHeadDim) : make_uint4(0, 0, 0, 0);
+    g[i] = on ? *reinterpret_cast<const uint4*>(p.d_o + off + i * kHeadDim) : make_uint4(0, 0, 0, 0);
+    l[i] = on ? p.lse[((size_t)b * p.n_heads + h0 + i) * p.seq + s] : -inf();
   }
 #pragma unroll
   for (int i = 0; i < kRowHeads; ++i) {

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kQkBwdThreads, kQkCtas)
 
 // dgain[c] = sum of the CTAs' partial sums: a block takes 16 of the 256 columns, 16 groups of threads every
 // 16th CTA each, and adds the groups in order.
-__global__ void __launch_bounds__(256) qk_gain_sum_kernel(const float* __restrict__ partial, int n,
+__global__ void __launch_bounds__(256) qk_gain_sum_kernel(const float* partial, int n,
                                                           float* __restrict__ dwq, float* __restrict__ dwk) {
   __shared__ float sums[16][17];
   grid_dep_wait();
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(256) qk_gain_sum_kernel(const float* __restric
   const int c = blockIdx.x * 16 + col;
   float t = 0.0f;
 #pragma unroll 8
-  for (int i = grp; i < n; i += 16) t += partial[(size_t)i * 256 + c];
+  for (int i = grp; i < n; i += 16) t += __ldcg(partial + (size_t)i * 256 + c);
   sums[grp][col] = t;
   __syncthreads();
   if (grp == 0) {

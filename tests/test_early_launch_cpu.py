@@ -41,6 +41,19 @@ def test_no_read_only_loads(name):
         assert not re.search(r"const[^,]*\*\s*__restrict__", params), kernel
 
 
+@pytest.mark.parametrize("file,names", [("attention.cu", ["attn_prepare_kernel", "attn_fwd_kernel"]),
+                                        ("attention_bwd.cu", ["attn_bwd_rows_kernel", "attn_bwd_kernel"]),
+                                        ("elementwise.cu", ["qk_gain_sum_kernel"])])
+def test_the_attention_pass(file, names):
+    """The attention's output and its log-sum-exp, the output's gradient, the gains' parts: the call before has just written them."""
+    with open(os.path.join(CSRC, file)) as f:
+        early = {k: (params, body) for k, params, body in _early(f.read())}
+    for kernel in names:
+        params, body = early[kernel]
+        assert not READ_ONLY.search(body), kernel
+        assert not re.search(r"const[^,]*\*\s*__restrict__", params), kernel
+
+
 def test_the_search_finds_them():
     text = """
     __global__ void f(const float* __restrict__ p, float* o) {  // __ldg(
