@@ -367,7 +367,7 @@ cudaError_t norm_bwd_start(const NormBwdArgs& a, const Plan& p, int parts, bool 
 
 template <typename T, int V, int E, int kWarps, bool kRms, bool kResidual>
 cudaError_t norm_bwd_width(const NormBwdArgs& a, const Plan& p, int parts, bool sums, cudaStream_t s) {
-  if constexpr (E == 8 || (E == 16 && V >= 4))  // (wider pieces come with wide rows only)
+  if constexpr ((E == 8 && !kRms) || (E == 16 && V >= 4))  // (wider pieces come with wide rows only, and 8 columns with rms)
     if (p.row_warps == 1) return norm_bwd_start<T, V, E, kWarps, false, kRms, kResidual>(a, p, parts, sums, s);
   if (!wide_plan(p)) return cudaErrorInvalidConfiguration;
   return norm_bwd_start<T, V, E, kWarps, true, kRms, kResidual>(a, p, parts, sums, s);
@@ -390,8 +390,10 @@ cudaError_t norm_bwd_run(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
       parts = p.cluster;
       second = false;
     }
-    const cudaError_t e = a.residual != nullptr ? norm_bwd_width<T, V, E, kWarps, kRms, true>(a, p, parts, sums, s)
-                                                : norm_bwd_width<T, V, E, kWarps, kRms, false>(a, p, parts, sums, s);
+    cudaError_t e = cudaErrorInvalidConfiguration;
+    if (a.residual != nullptr) e = norm_bwd_width<T, V, E, kWarps, kRms, true>(a, p, parts, sums, s);
+    else if constexpr (!(kRms && E == 8))  // (rms has 8 columns a lane with a residual only)
+      e = norm_bwd_width<T, V, E, kWarps, kRms, false>(a, p, parts, sums, s);
     if (e != cudaSuccess) return e;
   }
   if (!second) return cudaSuccess;

@@ -401,8 +401,8 @@ inline bool wide_plan(const Plan& p) { return p.row_warps > 1 && p.row_warps <= 
 // 14.0; 16418 x 4096 50.9, 51.5, 51.6, 52.8, 53.0; 3 x 10571 x 1792 rms backward, then with 8 columns a lane,
 // 65.3, 65.2, 63.9, 64.7, 66.5).
 constexpr int kFlight = 48 * 1024;
-constexpr int depth_of(int inputs, int turn, int held = 0) {  // held: rows that are kept beside the one that has come
-  const int want = 1 + held + (kFlight + inputs * turn - 1) / (inputs * turn), fit = kRingBytes / (inputs * turn);
+constexpr int depth_of(int inputs, int turn) {
+  const int want = 1 + (kFlight + inputs * turn - 1) / (inputs * turn), fit = kRingBytes / (inputs * turn);
   return want < fit ? want : fit;
 }
 
