@@ -10,13 +10,12 @@
 // A tensor may begin anywhere: the elements in front of its first and behind its last 16-byte boundary go with its first and
 // last item, one by one.  Where a gradient and the tensor that takes it clipped lie differently to those boundaries, the
 // clipping goes element by element.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
 #include "../../include/mi_block.h"
 #include "mi_internal.h"
 #include "ptx.cuh"
+#include "values.cuh"
 
 namespace mi {
 
@@ -55,15 +54,22 @@ struct Item {
   }
 };
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, __half& o) { o = __float2half_rn(v); }
 __device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
 // A vector as pairs in fp32, and back (rounded once).
-template <typename T> struct Vec;
+template <typename T> struct Vec {
+  static constexpr int N = 4;
+  __device__ __forceinline__ static void unpack(const uint4& v, f32x2_t (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = unpack2<T>(w[i]);
+  }
+  __device__ __forceinline__ static uint4 pack(const f32x2_t (&f)[4]) {
+    return make_uint4(pack2<T>(f[0]), pack2<T>(f[1]), pack2<T>(f[2]), pack2<T>(f[3]));
+  }
+};
 template <> struct Vec<float> {
   static constexpr int N = 2;
   __device__ __forceinline__ static void unpack(const uint4& v, f32x2_t (&f)[2]) {
@@ -77,63 +83,17 @@ template <> struct Vec<float> {
     return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
   }
 };
-template <> struct Vec<__nv_bfloat16> {
-  static constexpr int N = 4;
-  __device__ __forceinline__ static void unpack(const uint4& v, f32x2_t (&f)[4]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = f2_pack(bf16_lo(w[i]), bf16_hi(w[i]));
-  }
-  __device__ __forceinline__ static uint4 pack(const f32x2_t (&f)[4]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      f2_unpack(f[i], lo, hi);
-      w[i] = pack_bf16x2(lo, hi);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <> struct Vec<__half> {
-  static constexpr int N = 4;
-  __device__ __forceinline__ static void unpack(const uint4& v, f32x2_t (&f)[4]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[i] = f2_pack(t.x, t.y);
-    }
-  }
-  __device__ __forceinline__ static uint4 pack(const f32x2_t (&f)[4]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      f2_unpack(f[i], lo, hi);
-      const __half2 h = __floats2half2_rn(lo, hi);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-
-__device__ __forceinline__ float load(const void* p, int dtype, long long i) {
-  if (dtype == MI_F32) return static_cast<const float*>(p)[i];
-  if (dtype == MI_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
 
 // An item whose squares may leave fp32's range, again: a lane's elements times a power of two, whose square the sum is
-// divided by.  s: the lane's sum as it was.
-__device__ __noinline__ double item_squares_scaled(const void* grad, int dtype, long long i0, long long i1, float s) {
-  const float up = s <= kSmallest ? 0x1p100f : 0x1p-100f;
+// divided by.  top: the warp's largest sum as it was (infinity for NaN; 0 where all were too small).
+__device__ __noinline__ double item_squares_scaled(const void* grad, int dtype, long long i0, long long i1, float top) {
+  const float up = top <= kSmallest ? 0x1p100f : 0x1p-100f;
   float z = 0.0f;
   for (long long i = i0 + (threadIdx.x & 31); i < i1; i += 32) {
-    const float v = load(grad, dtype, i) * up;
+    const float v = value_at(grad, dtype, i, 0.0f) * up;
     z = fmaf(v, v, z);
   }
-  return (double)z * (s <= kSmallest ? 0x1p-200 : 0x1p200);  // (NaN stays)
+  return (double)z * (top <= kSmallest ? 0x1p-200 : 0x1p200);  // (NaN stays)
 }
 
 // A lane's part of an item's sum of squares, in 64 bits.  Up to 65 squares are added in 32 bits; where a lane's sum may have
@@ -230,7 +190,7 @@ __device__ __forceinline__ float clip_factor(float max_norm, float norm) {
 
 __device__ __noinline__ void scale_elements(const GradEntry& e, long long i0, long long i1, float c) {
   for (long long i = i0 + (threadIdx.x & 31); i < i1; i += 32) {
-    const float v = load(e.grad, e.dtype, i) * c;
+    const float v = value_at(e.grad, e.dtype, i, 0.0f) * c;
     if (e.dtype == MI_F32) static_cast<float*>(e.out)[i] = v;
     else if (e.dtype == MI_F16) static_cast<__half*>(e.out)[i] = __float2half_rn(v);
     else static_cast<__nv_bfloat16*>(e.out)[i] = __float2bfloat16_rn(v);

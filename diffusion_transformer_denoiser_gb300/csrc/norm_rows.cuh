@@ -20,13 +20,10 @@
 // cheaper ends 34 / 46.
 #pragma once
 
-#include <cuda_fp16.h>
-
-#include <type_traits>
-
 #include "../../include/mi_block.h"
 #include "mi_internal.h"
 #include "ptx.cuh"
+#include "values.cuh"
 
 namespace mi {
 
@@ -53,30 +50,6 @@ __device__ __forceinline__ bool v_any(f32x2_t a) { return (a & 0x7fffffff7ffffff
 template <typename L> __device__ __forceinline__ L v_of(float a);
 template <> __device__ __forceinline__ float v_of<float>(float a) { return a; }
 template <> __device__ __forceinline__ f32x2_t v_of<f32x2_t>(float a) { return f2_of(a); }
-
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// Two 16-bit values in a word as fp32, and back (rounded once).
-template <typename T> __device__ __forceinline__ f32x2_t unpack2(uint32_t w) {
-  if constexpr (std::is_same<T, __half>::value) {
-    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    return f2_pack(t.x, t.y);
-  } else {
-    return f2_pack(bf16_lo(w), bf16_hi(w));
-  }
-}
-template <typename T> __device__ __forceinline__ uint32_t pack2(f32x2_t v) {
-  float lo, hi;
-  f2_unpack(v, lo, hi);
-  if constexpr (std::is_same<T, __half>::value) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    return pack_bf16x2(lo, hi);
-  }
-}
 
 // Copies `bytes` of 16 and fills up with zeros (0: nothing is read).
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t bytes) {
@@ -165,14 +138,6 @@ template <typename L> __device__ __forceinline__ L v_of2(float a, float b) {
   else return a;
 }
 
-// Entry i of a parameter of the given type; p null: `none`.
-__device__ __forceinline__ float param_at(const void* p, int dtype, long long i, float none) {
-  if (p == nullptr) return none;
-  if (dtype == MI_F32) return static_cast<const float*>(p)[i];
-  if (dtype == MI_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
 // A lane's V columns from col on of a parameter, `plus` added (zeros past the width).  T: the rows' type, which the
 // parameter has unless it is fp32; aligned: the parameter is on a 16-byte boundary.
 template <typename T, int V>
@@ -201,7 +166,7 @@ __device__ __forceinline__ void load_param(const void* p, int dtype, bool aligne
   }
   float f[V];
 #pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = col + e < width ? param_at(p, dtype, at + col + e, none) + plus : 0.0f;
+  for (int e = 0; e < V; ++e) f[e] = col + e < width ? value_at(p, dtype, at + col + e, none) + plus : 0.0f;
 #pragma unroll
   for (int i = 0; i < P::N; ++i) w[i] = V == 1 ? v_of<L>(f[0]) : v_of2<L>(f[(2 * i) % V], f[(2 * i + 1) % V]);
 }

@@ -32,7 +32,7 @@ def _early(text):
     return [f for f in _kernels(text) if "grid_dep_wait()" in f[2]]
 
 
-@pytest.mark.parametrize("name", ["norm_rows.cuh", "layer_norm.cu", "norm_bwd.cu", "grads.cu"])
+@pytest.mark.parametrize("name", ["values.cuh", "norm_rows.cuh", "layer_norm.cu", "norm_bwd.cu", "grads.cu"])
 def test_no_read_only_loads(name):
     with open(os.path.join(CSRC, name)) as f:
         text = f.read()
