@@ -406,8 +406,8 @@ cudaError_t norm_bwd_run(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
 // residual: width 2560 55 against 72 for 8 with 16, 4096 56 / 62; rms without: 2560 43 against 49 for 8 with 24, 4096 44 / 55).
 // rms: 8 with 24 where 16 would leave a quarter of the warps without a row and there is a residual's memory traffic to hide it
 // (width 2816 60 / 64, 3072 55 / 57; without a residual 53 / 51, 47 / 45).  Odd rows of 16 bits: 8 up to three warps of them (16 M: width 515
-// 47 / 49, with a residual 56 / 65), then 16 (769 37 / 44, 1283 36 / 45, with one 43 / 53); of fp32: 8, whose copies leave room
-// for more rows on the way.  32 where these do not hold a row.
+// 47 / 49, with a residual 56 / 65), then 16 (769 37 / 44, 1283 36 / 45, with one 43 / 53); of fp32: 8 up to
+// 4096 columns, whose copies leave room for a row or two on the way.  32 where these do not hold a row.
 template <typename T, int V, bool kRms>
 cudaError_t norm_bwd_any(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
   if constexpr (kRms) {

@@ -476,9 +476,9 @@ mi_status mi_grads_workspace_size(const mi_grads* set, size_t* bytes);
  * ws: mi_grads_workspace_size bytes, 256-byte aligned; it holds nothing between calls. */
 mi_status mi_grad_norm(const mi_grads* set, float* norm, void* ws, size_t ws_bytes, void* stream);
 
-/* outs = grads * c, c = min(1, max_norm / (norm[0] + 1e-6)) in fp32, each product rounded once.  norm is read from the
- * device: mi_grad_norm's, or one that the caller has put together from several sets or GPUs.  With c = 1 tensors that are
- * clipped in place are left as they are.  norm = infinity gives c = 0 (and NaN where a gradient is infinite), a NaN gives
+/* outs = grads * c, c = min(1, max_norm / (norm[0] + 1e-6)): both and their product in fp32, which is then rounded to the
+ * output's type.  norm is read from the device: mi_grad_norm's, or one that the caller has put together from several
+ * sets or GPUs.  With c = 1 tensors that are clipped in place are left as they are.  norm = infinity gives c = 0 (and NaN where a gradient is infinite), a NaN gives
  * NaN everywhere, so a bad step does not pass unseen.  0 < max_norm < infinity. */
 mi_status mi_grad_clip(const mi_grads* set, float max_norm, const float* norm, void* stream);
 
