@@ -421,9 +421,9 @@ typedef enum mi_dtype {
  *   mean, rstd  fp32 [rows], for mi_layer_norm_backward, or NULL
  * 1 <= width <= MI_NORM_MAX_WIDTH; rows may be 0 (nothing happens).  The row's mean is taken off before it is
  * squared, and what its rounding leaves after it, in fp32, so a row far from zero loses nothing in out and rstd: 100000.1
- * everywhere gives the bias.  mean itself is rounded to fp32.  Sums and squares are fp32: |x - m| from 2^63 on leaves their range.
- * A row with an infinity or NaN gives NaN.  Outputs that overlap x, the weights or each other are refused (rows that
- * interleave without touching are fine). */
+ * everywhere gives the bias.  mean itself is rounded to fp32.  Sums and squares are fp32, which holds them for |x| below 2^66
+ * and |x - m| below 2^50; a row beyond that may give NaN, and one with an infinity or NaN does.  Outputs that overlap x, the
+ * weights or each other are refused (rows that interleave without touching are fine). */
 #define MI_NORM_MAX_WIDTH 16384
 mi_status mi_layer_norm(const void* x, int64_t x_stride, const void* weight, const void* bias, void* out, int64_t out_stride,
                         float* mean, float* rstd, int rows, int width, float eps, int dtype, int param_dtype, void* stream);

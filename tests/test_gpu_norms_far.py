@@ -68,3 +68,16 @@ def test_small_spread_far_from_zero(width, kind):
         n.x.t.copy_(at.double().cuda() + step * torch.randint(-3, 4, (37, width), generator=g, device="cuda"))
         n.forward(mi)
         _check(n, 1e-6)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_the_largest_values_that_are_promised(width, kind):
+    """|x| just below 2^66, deviations just below 2^50 (bf16: no smaller ones than steps of 2^58 there, so |x| below 2^50)."""
+    mi = require_gpu()
+    n = Norm(37, width, kind)
+    g = torch.Generator(device="cuda").manual_seed(width)
+    at = 2.0 ** 65.9 if kind == "f32" else 0.0
+    n.x.t.copy_(at + (2 * torch.rand(37, width, generator=g, device="cuda", dtype=torch.float64) - 1) * 2.0 ** 48.9)
+    n.forward(mi)
+    _check(n, 1e-6)
